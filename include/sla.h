@@ -318,6 +318,83 @@ sla_status sla_stage_timing(int max_calls);
  * *calls, then clears the record (recording continues). */
 sla_status sla_stage_times(float* ms, int* calls);
 
+/* ---------------------------------------------------------------------------
+ * Operators before and beside the attention: rotary positions, the norm of
+ * every query and key head with the rotation in the same pass, and exact
+ * attention over packed prompts. They keep the conventions above (host
+ * validation, asynchronous on the given stream, no allocation, deterministic
+ * results), but take strided tensors. They were added to ABI version 5 without
+ * changing anything in it.
+ * ------------------------------------------------------------------------- */
+
+typedef enum { SLA_BF16 = 0, SLA_FP16 = 1, SLA_FP32 = 2 } sla_dtype;
+
+/* Head rows of a [B, H, N, d] tensor in any memory order: element (b, h, n, i)
+ * is at base + b sb + h sh + n sn + i (strides in elements). Inputs may repeat
+ * rows (stride 0); rows of an output must be distinct memory. An output may be
+ * its own input (same base and strides); other overlaps are undefined. */
+typedef struct sla_heads {
+  void* base;
+  int H;
+  long long sb, sh, sn;
+} sla_heads;
+
+typedef enum {
+  SLA_ROPE_INTERLEAVED = 0, /* pair i is (x[2i], x[2i + 1]) */
+  SLA_ROPE_HALF = 1         /* pair i is (x[i], x[i + rot_dim / 2]) */
+} sla_rope_layout;
+
+/* A rotation: pair i of the first rot_dim values of a row turns by the angle
+ * p f_i, p the integer position of the row's token on the pair's axis, and is
+ * scaled by gain; the values behind rot_dim pass unchanged.
+ *   turns  [rot_dim / 2] device, uint64: round(2^64 f_i / 2 pi) mod 2^64. The
+ *          angle is formed by one product mod 2^64, exact at any position.
+ *   axis   [rot_dim / 2] device, uint8: the pair's axis (n_axes - 1 where it is
+ *          larger); NULL: axis 0.
+ *   pos    device int32 (pos_bits = 32) or int64 (64): the position of token
+ *          (b, n) on axis a is pos[a pos_axis + b pos_b + n pos_n] (any value,
+ *          negative too); NULL: n on every axis. */
+typedef struct sla_rope_spec {
+  const unsigned long long* turns;
+  const unsigned char* axis;
+  const void* pos;
+  long long pos_axis, pos_b, pos_n;
+  float gain; /* factor on cos and sin: 1, or a context scaling's attention factor */
+  int pos_bits;
+  int rot_dim; /* even, 0 .. d */
+  int layout;  /* sla_rope_layout */
+  int n_axes;  /* 1 .. 255 */
+} sla_rope_spec;
+
+/* y = x rotated (inverse != 0: by the negative angles, the gradient of the
+ * rotation). x and y have the same H; rows n < N of every (b, h) are written.
+ * d even, 2 .. 256; B N < 2^31. Computed in float32, rounded once.
+ * Errors: SLA_ERR_INVALID_ARG (null or bad sizes, an output with repeated rows),
+ * SLA_ERR_UNSUPPORTED (d, too many tokens or heads), SLA_ERR_ALIGNMENT (an
+ * address not a multiple of its type's size). */
+sla_status sla_rope(const sla_heads* x, const sla_heads* y, int B, int N, int d, int dtype,
+                    const sla_rope_spec* rope, int inverse, void* stream);
+
+/* yq = rope(q / sqrt(mean(q^2) + eps) * wq), yk likewise from k and wk, the
+ * mean over the d values of each head row; one launch for both.
+ *   wq, wk  [d] device, of the tensors' dtype, or float32 where w_f32 != 0.
+ *   rope    NULL: the norm alone. */
+sla_status sla_qk_norm_rope(const sla_heads* q, const sla_heads* k, const void* wq, const void* wk, int w_f32,
+                            float eps, const sla_heads* yq, const sla_heads* yk, int B, int N, int d, int dtype,
+                            const sla_rope_spec* rope, void* stream);
+
+/* Bytes of workspace of sla_qk_norm_rope_backward (0 for invalid sizes). */
+size_t sla_qk_norm_rope_backward_workspace_size(int B, int N, int Hq, int Hk, int d);
+
+/* Gradients of <dyq, yq> + <dyk, yk>: dq, dk (rows n < N), and dwq, dwk ([d]
+ * float32 device; both may be NULL). The norm is formed again from q and k.
+ * workspace: 16-byte aligned device scratch. */
+sla_status sla_qk_norm_rope_backward(const sla_heads* q, const sla_heads* k, const void* wq, const void* wk,
+                                     int w_f32, float eps, const sla_heads* dyq, const sla_heads* dyk,
+                                     const sla_heads* dq, const sla_heads* dk, float* dwq, float* dwk, int B, int N,
+                                     int d, int dtype, const sla_rope_spec* rope, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -39,7 +39,8 @@ EXPORTS = ("sla_abi_version", "sla_status_string", "sla_validate", "sla_workspac
            "sla_forward", "sla_get_mask", "sla_get_pooled", "sla_read_device_status",
            "sla_dense_forward", "sla_stage_timing", "sla_stage_times", "sla_forward_noalloc",
            "sla_get_quantized", "sla_router_soft_topk", "sla_forward_train", "sla_backward_workspace_size",
-           "sla_backward", "sla_check_wait_timeout")
+           "sla_backward", "sla_check_wait_timeout",
+           "sla_rope", "sla_qk_norm_rope", "sla_qk_norm_rope_backward_workspace_size", "sla_qk_norm_rope_backward")
 NOALLOC_WORKSPACE_BYTES = 32 << 20
 NUM_STAGES = 6
 STAGES = ("pool", "phik_hz", "scores", "classify", "hz_reduce", "attention")
@@ -65,6 +66,20 @@ class Saved(ctypes.Structure):
                 ("den", ctypes.c_void_p)]
 
 
+class Heads(ctypes.Structure):
+    """Mirror of struct sla_heads."""
+    _fields_ = [("base", ctypes.c_void_p), ("H", ctypes.c_int), ("sb", ctypes.c_longlong),
+                ("sh", ctypes.c_longlong), ("sn", ctypes.c_longlong)]
+
+
+class RopeSpec(ctypes.Structure):
+    """Mirror of struct sla_rope_spec."""
+    _fields_ = [("turns", ctypes.c_void_p), ("axis", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("pos_axis", ctypes.c_longlong), ("pos_b", ctypes.c_longlong), ("pos_n", ctypes.c_longlong),
+                ("gain", ctypes.c_float), ("pos_bits", ctypes.c_int), ("rot_dim", ctypes.c_int),
+                ("layout", ctypes.c_int), ("n_axes", ctypes.c_int)]
+
+
 class SLAError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -84,6 +99,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     vp, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
     P = ctypes.POINTER(Params)
+    f, HP, RP = ctypes.c_float, ctypes.POINTER(Heads), ctypes.POINTER(RopeSpec)
     sig = {
         "sla_abi_version": (i, []),
         "sla_status_string": (ctypes.c_char_p, [i]),
@@ -101,6 +117,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sla_backward_workspace_size": (sz, [P]),
         "sla_backward": (i, [vp, vp, vp, vp, P, ctypes.POINTER(Saved), vp, sz, vp, vp, vp, vp, vp, vp, sz, vp]),
         "sla_check_wait_timeout": (i, [vp, sz, ctypes.c_longlong, vp]),
+        "sla_rope": (i, [HP, HP, i, i, i, i, RP, i, vp]),
+        "sla_qk_norm_rope": (i, [HP, HP, vp, vp, i, f, HP, HP, i, i, i, i, RP, vp]),
+        "sla_qk_norm_rope_backward_workspace_size": (sz, [i, i, i, i, i]),
+        "sla_qk_norm_rope_backward": (i, [HP, HP, vp, vp, i, f, HP, HP, HP, HP, vp, vp, i, i, i, i, RP, vp, sz, vp]),
         "sla_stage_timing": (i, [i]),
         "sla_stage_times": (i, [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int)]),
     }
@@ -392,3 +412,6 @@ def attention(q, k, v, *, N: Optional[int] = None, variant: str = "sla", k_crit:
             return dq, dk, dv, dw, da
 
     return _SLAFunction.apply(q, k, v, w_proj, alpha)
+
+
+from .rope import RopeTable, qk_norm_rope, qk_norm_rope_backward, rope, rope_table  # noqa: E402,F401
