@@ -395,6 +395,59 @@ sla_status sla_qk_norm_rope_backward(const sla_heads* q, const sla_heads* k, con
                                      int d, int dtype, const sla_rope_spec* rope, void* workspace,
                                      size_t workspace_bytes, void* stream);
 
+/* Exact attention over packed prompts: n_seq sequences of tokens behind one
+ * another, query heads in groups that share a key head, causal or full.
+ *   O = softmax(scale Q K^T + mask) V per sequence and head; query head h reads
+ *   key head h / (Hq / Hkv). Causal: query i of a sequence sees its keys
+ *   0 .. len_k - len_q + i (its last query sits at its last key: a whole prompt,
+ *   a piece of a prompt behind what a cache holds, single tokens over caches).
+ *   A query that sees no key gets O = 0 and lse = -inf.
+ * Tokens are rows: element (t, h, i) of a tensor is at base + t row + h head + i
+ * (strides in elements, multiples of 8 on axes longer than one; base 16-byte
+ * aligned), bf16. Rows behind the last sequence are neither read into any result
+ * nor written, and no sequence reads another's rows into its results (they may
+ * hold NaN). Within a sequence, a key or value row that is not finite reaches
+ * every query that sees it, and may reach queries before it in the same block of
+ * 128 keys.
+ *
+ * The sequences' lengths are planned once on the host: a plan lists the kernels'
+ * work items, the longest first. sla_prompt_plan writes it to host memory; the
+ * caller copies the same bytes to the device (256-byte aligned) and passes both.
+ * One plan serves any number of calls, also at the same time; only the device
+ * copy's status word (sla_read_device_status(plan_device, stream)) is written to,
+ * and only when a bounded in-kernel wait expires or an item is out of range. */
+typedef struct sla_prompt_params {
+  int n_seq;             /* >= 1 */
+  const int32_t* len_q;  /* HOST [n_seq], each >= 0; at least one token in all */
+  const int32_t* len_k;  /* HOST [n_seq] or NULL: the same as len_q */
+  int Hq, Hkv;           /* Hq a multiple of Hkv, Hq / Hkv <= 128 */
+  int d;                 /* 64 or 128 */
+  int causal;            /* 0 or 1 */
+  float softmax_scale;   /* 0 selects 1/sqrt(d) */
+} sla_prompt_params;
+
+typedef struct sla_rows {
+  void* base;
+  long long row, head;
+} sla_rows;
+
+/* SLA_OK, or why these parameters are refused. */
+sla_status sla_prompt_validate(const sla_prompt_params* p);
+
+/* Bytes of the plan (0 for invalid parameters), and the plan itself. */
+size_t sla_prompt_plan_size(const sla_prompt_params* p);
+sla_status sla_prompt_plan(const sla_prompt_params* p, void* plan, size_t plan_bytes);
+
+/* Bytes of device workspace of sla_prompt_forward (0: none needed; it is used
+ * where few rows read long caches, whose keys are then split among blocks). */
+size_t sla_prompt_workspace_size(const void* plan);
+
+/* O and, where lse is not NULL, lse [Tq, Hq] float32 = log sum exp(scale q.k)
+ * over the keys that each query sees (what the backward reads). */
+sla_status sla_prompt_forward(const sla_rows* q, const sla_rows* k, const sla_rows* v, const sla_rows* o, float* lse,
+                              const void* plan, size_t plan_bytes, void* plan_device, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

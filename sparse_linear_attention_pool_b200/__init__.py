@@ -40,7 +40,9 @@ EXPORTS = ("sla_abi_version", "sla_status_string", "sla_validate", "sla_workspac
            "sla_dense_forward", "sla_stage_timing", "sla_stage_times", "sla_forward_noalloc",
            "sla_get_quantized", "sla_router_soft_topk", "sla_forward_train", "sla_backward_workspace_size",
            "sla_backward", "sla_check_wait_timeout",
-           "sla_rope", "sla_qk_norm_rope", "sla_qk_norm_rope_backward_workspace_size", "sla_qk_norm_rope_backward")
+           "sla_rope", "sla_qk_norm_rope", "sla_qk_norm_rope_backward_workspace_size", "sla_qk_norm_rope_backward",
+           "sla_prompt_validate", "sla_prompt_plan_size", "sla_prompt_plan", "sla_prompt_workspace_size",
+           "sla_prompt_forward")
 NOALLOC_WORKSPACE_BYTES = 32 << 20
 NUM_STAGES = 6
 STAGES = ("pool", "phik_hz", "scores", "classify", "hz_reduce", "attention")
@@ -80,6 +82,18 @@ class RopeSpec(ctypes.Structure):
                 ("layout", ctypes.c_int), ("n_axes", ctypes.c_int)]
 
 
+class PromptParams(ctypes.Structure):
+    """Mirror of struct sla_prompt_params (len_q, len_k: host addresses)."""
+    _fields_ = [("n_seq", ctypes.c_int), ("len_q", ctypes.c_void_p), ("len_k", ctypes.c_void_p),
+                ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("causal", ctypes.c_int),
+                ("softmax_scale", ctypes.c_float)]
+
+
+class Rows(ctypes.Structure):
+    """Mirror of struct sla_rows."""
+    _fields_ = [("base", ctypes.c_void_p), ("row", ctypes.c_longlong), ("head", ctypes.c_longlong)]
+
+
 class SLAError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -99,6 +113,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     vp, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
     P = ctypes.POINTER(Params)
+    PP, TP = ctypes.POINTER(PromptParams), ctypes.POINTER(Rows)
     f, HP, RP = ctypes.c_float, ctypes.POINTER(Heads), ctypes.POINTER(RopeSpec)
     sig = {
         "sla_abi_version": (i, []),
@@ -121,6 +136,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sla_qk_norm_rope": (i, [HP, HP, vp, vp, i, f, HP, HP, i, i, i, i, RP, vp]),
         "sla_qk_norm_rope_backward_workspace_size": (sz, [i, i, i, i, i]),
         "sla_qk_norm_rope_backward": (i, [HP, HP, vp, vp, i, f, HP, HP, HP, HP, vp, vp, i, i, i, i, RP, vp, sz, vp]),
+        "sla_prompt_validate": (i, [PP]),
+        "sla_prompt_plan_size": (sz, [PP]),
+        "sla_prompt_plan": (i, [PP, vp, sz]),
+        "sla_prompt_workspace_size": (sz, [vp]),
+        "sla_prompt_forward": (i, [TP, TP, TP, TP, vp, vp, sz, vp, vp, sz, vp]),
         "sla_stage_timing": (i, [i]),
         "sla_stage_times": (i, [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int)]),
     }
@@ -414,4 +434,5 @@ def attention(q, k, v, *, N: Optional[int] = None, variant: str = "sla", k_crit:
     return _SLAFunction.apply(q, k, v, w_proj, alpha)
 
 
+from .prompt import PromptPlan, prompt_attention, prompt_forward, prompt_plan  # noqa: E402,F401
 from .rope import RopeTable, qk_norm_rope, qk_norm_rope_backward, rope, rope_table  # noqa: E402,F401

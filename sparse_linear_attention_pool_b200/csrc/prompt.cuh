@@ -1,0 +1,65 @@
+// Packed prompt attention: the plan (one block of bytes, the same on host and
+// device) and the launchers.
+#pragma once
+
+#include "sla_internal.cuh"
+
+namespace sla {
+
+constexpr int kPromptTile = 128;  // packed query rows and keys per tile
+constexpr int kPromptSms = 148;
+
+// A packed query tile holds tpt = 128 / G whole tokens: row t G + g is token t,
+// query head (key head) G + g. The G heads that share a key head so share its
+// tiles, and single tokens fill a tile as far as they can.
+struct PromptItem {
+  int q0, nq;    // first query token (row of the packed tensor), tokens
+  int k0, lk;    // first key row and number of keys of the sequence
+  int pos0;      // causal: query token q0 + i sees keys 0 .. pos0 + i (full: unused)
+  int head;      // key head
+  int b0, b1;    // key blocks of 128 [b0, b1) that this item reads
+  int slot;      // < 0: writes O itself; else the slot of its partial result
+  int pad[3];
+};
+// Rows whose keys were split: slots first .. first + n - 1 are joined.
+struct PromptJoin {
+  int q0, nq, head, first, n, pad[3];
+};
+// A tile of 128 keys of one key head (dK, dV): the query tiles [t0, t1) of its sequence.
+struct PromptKeys {
+  int k0, lk;    // first key row of the sequence, its keys
+  int q0, lq;    // first query token of the sequence, its tokens
+  int block;     // key block
+  int head;
+  int t0, t1;
+};
+
+struct PromptPlan {
+  int status;  // device copy: the status word
+  unsigned magic;
+  int n_seq, Hq, Hkv, G, d, causal;
+  float scale;
+  int tiles;   // query tiles per forward item (1 or 2)
+  long long Tq, Tk;
+  int n_items, n_joins, n_slots, n_keys, n_rows;  // n_rows: dQ items
+  unsigned long long items, joins, keys, rows, total;  // byte offsets
+};
+constexpr unsigned kPromptMagic = 0x534c4131u;
+
+struct PromptMaps;
+struct PromptTensor {
+  void* base;
+  long long row, head;
+};
+
+struct PromptArgs {
+  const PromptPlan* plan;     // host
+  unsigned char* plan_dev;
+  PromptTensor q, k, v, o;
+  float* lse;                 // [Tq, Hq] or null
+  float* part;                // [slots][tiles 128][d] partial O
+  float* part_lse;            // [slots][tiles 128], log2
+};
+cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s);
+
+}  // namespace sla

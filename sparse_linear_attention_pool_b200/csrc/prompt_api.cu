@@ -1,0 +1,289 @@
+// C ABI of the packed prompt attention (declared in include/sla.h): validation,
+// the plan of work items, and the calls.
+//
+// The plan is made on the host because the lengths are known there: no kernel has
+// to search for its sequence, the longest items start first (blocks are dispatched
+// in order, so this is longest-processing-time scheduling over the SMs), and the
+// keys of long caches are split where the rows alone would leave SMs idle.
+#include <math.h>
+#include <string.h>
+
+#include <functional>
+#include <queue>
+#include <vector>
+
+#include "prompt.cuh"
+
+using namespace sla;
+
+namespace {
+
+sla_status check_params(const sla_prompt_params* p) {
+  if (p == nullptr || p->n_seq < 1 || p->len_q == nullptr) return SLA_ERR_INVALID_ARG;
+  if (p->Hq < 1 || p->Hkv < 1 || p->Hq % p->Hkv != 0) return SLA_ERR_INVALID_ARG;
+  if (p->causal != 0 && p->causal != 1) return SLA_ERR_INVALID_ARG;
+  if (!(p->softmax_scale >= 0.0f) || isinf(p->softmax_scale)) return SLA_ERR_INVALID_ARG;
+  if (p->d != 64 && p->d != 128) return SLA_ERR_UNSUPPORTED;
+  if (p->Hq / p->Hkv > 128 || p->Hq > 65535) return SLA_ERR_UNSUPPORTED;
+  long long tq = 0, tk = 0;
+  for (int i = 0; i < p->n_seq; ++i) {
+    const int lq = p->len_q[i], lk = p->len_k ? p->len_k[i] : lq;
+    if (lq < 0 || lk < 0) return SLA_ERR_INVALID_ARG;
+    tq += lq;
+    tk += lk;
+  }
+  if (tq < 1) return SLA_ERR_INVALID_ARG;
+  // rows, positions and tile ends are 32-bit in the kernels
+  if (tq > 0x7fffffffLL - 1024 || tk > 0x7fffffffLL - 1024) return SLA_ERR_UNSUPPORTED;
+  return SLA_OK;
+}
+
+struct Lists {
+  std::vector<PromptItem> items, rows;
+  std::vector<PromptJoin> joins;
+  std::vector<PromptKeys> keys;
+  int tiles = 2, slots = 0;
+};
+
+int key_blocks(const sla_prompt_params& p, int lq, int lk, int last_token) {
+  const long long keys = p.causal ? std::min<long long>(lk, (long long)lk - lq + last_token + 1) : lk;
+  return int((std::max(0LL, keys) + kPromptTile - 1) / kPromptTile);
+}
+
+// Items of `per` tokens, all key blocks each.
+std::vector<PromptItem> row_items(const sla_prompt_params& p, int per) {
+  std::vector<PromptItem> out;
+  int q0 = 0, k0 = 0;
+  for (int s = 0; s < p.n_seq; ++s) {
+    const int lq = p.len_q[s], lk = p.len_k ? p.len_k[s] : lq;
+    for (int t = 0; t < lq; t += per)
+      for (int h = 0; h < p.Hkv; ++h) {
+        PromptItem it{};
+        it.q0 = q0 + t;
+        it.nq = std::min(per, lq - t);
+        it.k0 = k0;
+        it.lk = lk;
+        it.pos0 = lk - lq + t;
+        it.head = h;
+        it.b1 = key_blocks(p, lq, lk, t + it.nq - 1);
+        it.slot = -1;
+        out.push_back(it);
+      }
+    q0 += lq;
+    k0 += lk;
+  }
+  return out;
+}
+
+// Time at which the last SM ends, blocks of cost (key blocks + overhead) dispatched longest first.
+double makespan(std::vector<double> cost) {
+  std::sort(cost.begin(), cost.end(), std::greater<double>());
+  std::priority_queue<double, std::vector<double>, std::greater<double>> sm;
+  for (int i = 0; i < kPromptSms; ++i) sm.push(0.0);
+  double last = 0.0;
+  for (double c : cost) {
+    const double e = sm.top() + c;
+    sm.pop();
+    sm.push(e);
+    last = std::max(last, e);
+  }
+  return last;
+}
+
+// Pieces that an item of n blocks is cut into for pieces of about `chunk` blocks.
+int pieces(int n, int chunk) { return chunk <= 0 || n <= chunk ? 1 : (n + chunk - 1) / chunk; }
+
+// Costs in units of one key block of a two-tile item.
+constexpr double kItemCost = 3.0;      // start, first loads and the store
+constexpr double kOneTile = 0.8;       // a step of a one-tile item
+constexpr double kJoinCost = 4.0;      // the second launch
+
+double split_cost(const std::vector<PromptItem>& items, int chunk, double step) {
+  std::vector<double> cost;
+  bool any = false;
+  for (const PromptItem& it : items) {
+    const int n = pieces(it.b1, chunk);
+    any = any || n > 1;
+    for (int i = 0; i < n; ++i) cost.push_back(kItemCost + step * ((it.b1 + n - 1) / n));
+  }
+  return makespan(cost) + (any ? kJoinCost : 0.0);
+}
+
+Lists make_lists(const sla_prompt_params& p) {
+  Lists L;
+  const int G = p.Hq / p.Hkv, tpt = kPromptTile / G;
+  int longest = 0;
+  for (int s = 0; s < p.n_seq; ++s) longest = std::max(longest, p.len_q[s]);
+  // Two tiles share every key tile and hide each other's softmax; one tile per
+  // item spreads little work over more SMs. Few items may also split their keys.
+  double best = 0.0;
+  int best_chunk = 0;
+  std::vector<PromptItem> base;
+  for (int tiles = longest <= tpt ? 1 : 2; tiles >= 1; --tiles) {
+    std::vector<PromptItem> items = row_items(p, tiles * tpt);
+    const double step = tiles == 2 ? 1.0 : kOneTile;
+    std::vector<int> chunks = {0};
+    if (items.size() < 4 * kPromptSms) {
+      long long total = 0;
+      for (const PromptItem& it : items) total += it.b1;
+      for (int w : {1, 2, 3, 4, 6}) chunks.push_back(int(std::max(4LL, total / (kPromptSms * w) + 1)));
+    }
+    for (int chunk : chunks) {
+      const double c = split_cost(items, chunk, step);
+      if (base.empty() || c < best) {
+        best = c;
+        best_chunk = chunk;
+        base = items;
+        L.tiles = tiles;
+      }
+    }
+    if (items.size() >= 4 * kPromptSms) break;  // enough two-tile items: one tile each cannot be better
+  }
+  for (const PromptItem& it : base) {
+    const int n = pieces(it.b1, best_chunk);
+    if (n == 1) {
+      L.items.push_back(it);
+      continue;
+    }
+    L.joins.push_back(PromptJoin{it.q0, it.nq, it.head, L.slots, n, {}});
+    for (int i = 0; i < n; ++i) {
+      PromptItem part = it;
+      part.b0 = int((long long)it.b1 * i / n);
+      part.b1 = int((long long)it.b1 * (i + 1) / n);
+      part.slot = L.slots++;
+      L.items.push_back(part);
+    }
+  }
+  auto longer = [](const PromptItem& a, const PromptItem& b) { return a.b1 - a.b0 > b.b1 - b.b0; };
+  std::stable_sort(L.items.begin(), L.items.end(), longer);
+  return L;
+}
+
+size_t layout(const sla_prompt_params& p, const Lists& L, PromptPlan* h) {
+  memset(h, 0, sizeof(*h));
+  h->magic = kPromptMagic;
+  h->n_seq = p.n_seq;
+  h->Hq = p.Hq;
+  h->Hkv = p.Hkv;
+  h->G = p.Hq / p.Hkv;
+  h->d = p.d;
+  h->causal = p.causal;
+  h->scale = p.softmax_scale > 0.0f ? p.softmax_scale : 1.0f / sqrtf(float(p.d));
+  h->tiles = L.tiles;
+  for (int i = 0; i < p.n_seq; ++i) {
+    h->Tq += p.len_q[i];
+    h->Tk += p.len_k ? p.len_k[i] : p.len_q[i];
+  }
+  h->n_items = int(L.items.size());
+  h->n_joins = int(L.joins.size());
+  h->n_slots = L.slots;
+  h->n_keys = int(L.keys.size());
+  h->n_rows = int(L.rows.size());
+  size_t off = align256(sizeof(PromptPlan));
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align256(off + bytes);
+    return o;
+  };
+  h->items = take(L.items.size() * sizeof(PromptItem));
+  h->joins = take(L.joins.size() * sizeof(PromptJoin));
+  h->keys = take(L.keys.size() * sizeof(PromptKeys));
+  h->rows = take(L.rows.size() * sizeof(PromptItem));
+  h->total = off;
+  return off;
+}
+
+const PromptPlan* plan_of(const void* plan, size_t bytes) {
+  if (plan == nullptr || reinterpret_cast<uintptr_t>(plan) % 8 != 0 || bytes < sizeof(PromptPlan)) return nullptr;
+  const PromptPlan* p = static_cast<const PromptPlan*>(plan);
+  return p->magic == kPromptMagic && p->total <= bytes ? p : nullptr;
+}
+
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// Address, strides (TMA: multiples of 16 bytes, below 2^40) and, for outputs, distinct rows.
+sla_status check_rows(const sla_rows* t, long long T, int H, int d, bool output, PromptTensor* out) {
+  if (t == nullptr || t->base == nullptr) return SLA_ERR_INVALID_ARG;
+  long long row = T > 1 ? t->row : (long long)d * H, head = H > 1 ? t->head : (long long)d;
+  if (row <= 0 || head <= 0) return SLA_ERR_INVALID_ARG;
+  if (row >= (1LL << 38) || head >= (1LL << 31)) return SLA_ERR_UNSUPPORTED;
+  if (output) {
+    const bool heads_inside = head >= d && (T == 1 || row >= head * (H - 1) + d);
+    const bool rows_inside = row >= d && (H == 1 || head >= row * (T - 1) + d);
+    if (!heads_inside && !rows_inside) return SLA_ERR_INVALID_ARG;
+  }
+  if (!aligned(t->base, 16) || row % 8 != 0 || head % 8 != 0) return SLA_ERR_ALIGNMENT;
+  *out = PromptTensor{t->base, row, head};
+  return SLA_OK;
+}
+
+size_t forward_workspace(const PromptPlan& p) {
+  return p.n_slots == 0 ? 0 : align256(size_t(p.n_slots) * p.tiles * 128 * (size_t(p.d) + 1) * sizeof(float));
+}
+
+sla_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (need == 0) return SLA_OK;
+  return ws == nullptr || !aligned(ws, 256) || have < need ? SLA_ERR_WORKSPACE : SLA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+sla_status sla_prompt_validate(const sla_prompt_params* p) { return check_params(p); }
+
+size_t sla_prompt_plan_size(const sla_prompt_params* p) {
+  if (check_params(p) != SLA_OK) return 0;
+  PromptPlan h;
+  return layout(*p, make_lists(*p), &h);
+}
+
+sla_status sla_prompt_plan(const sla_prompt_params* p, void* plan, size_t plan_bytes) {
+  const sla_status st = check_params(p);
+  if (st != SLA_OK) return st;
+  if (plan == nullptr) return SLA_ERR_INVALID_ARG;
+  if (!aligned(plan, 8)) return SLA_ERR_ALIGNMENT;
+  const Lists L = make_lists(*p);
+  PromptPlan h;
+  if (plan_bytes < layout(*p, L, &h)) return SLA_ERR_WORKSPACE;
+  unsigned char* out = static_cast<unsigned char*>(plan);
+  memset(out, 0, h.total);
+  memcpy(out, &h, sizeof(h));
+  auto put = [&](size_t at, const void* src, size_t bytes) {
+    if (bytes) memcpy(out + at, src, bytes);
+  };
+  put(h.items, L.items.data(), L.items.size() * sizeof(PromptItem));
+  put(h.joins, L.joins.data(), L.joins.size() * sizeof(PromptJoin));
+  put(h.keys, L.keys.data(), L.keys.size() * sizeof(PromptKeys));
+  put(h.rows, L.rows.data(), L.rows.size() * sizeof(PromptItem));
+  return SLA_OK;
+}
+
+size_t sla_prompt_workspace_size(const void* plan) {
+  const PromptPlan* p = plan_of(plan, ~size_t(0));
+  return p == nullptr ? 0 : forward_workspace(*p);
+}
+
+sla_status sla_prompt_forward(const sla_rows* q, const sla_rows* k, const sla_rows* v, const sla_rows* o, float* lse,
+                              const void* plan, size_t plan_bytes, void* plan_device, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  const PromptPlan* p = plan_of(plan, plan_bytes);
+  if (p == nullptr || plan_device == nullptr) return SLA_ERR_INVALID_ARG;
+  PromptArgs a{};
+  sla_status st = check_rows(q, p->Tq, p->Hq, p->d, false, &a.q);
+  if (st == SLA_OK) st = check_rows(o, p->Tq, p->Hq, p->d, true, &a.o);
+  if (st == SLA_OK && p->Tk > 0) st = check_rows(k, p->Tk, p->Hkv, p->d, false, &a.k);
+  if (st == SLA_OK && p->Tk > 0) st = check_rows(v, p->Tk, p->Hkv, p->d, false, &a.v);
+  if (st != SLA_OK) return st;
+  if (!aligned(plan_device, 256) || !aligned(lse, 4)) return SLA_ERR_ALIGNMENT;
+  st = check_workspace(workspace, workspace_bytes, forward_workspace(*p));
+  if (st != SLA_OK) return st;
+  a.plan = p;
+  a.plan_dev = static_cast<unsigned char*>(plan_device);
+  a.lse = lse;
+  a.part = static_cast<float*>(workspace);
+  a.part_lse = a.part + size_t(p->n_slots) * p->tiles * 128 * p->d;
+  return launch_prompt_forward(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SLA_OK : SLA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,463 @@
+// Packed prompt attention, forward: softmax(scale Q K^T + mask) V on tcgen05.
+//
+// One CTA per item: up to two tiles of 128 packed query rows (A: tile 0, B: tile
+// 1) against the key blocks b1 - 1 .. b0 of one key head, the masked diagonal
+// first. One pass with a running maximum and sum per row:
+//   S = Q K_j^T (M = N = 128, K = d)          -> TMEM, one buffer per tile
+//   m' = max(m, rowmax S), P = 2^(c S - c m'), l = l 2^(c m - c m') + rowsum P
+//   O = O 2^(c m - c m') + P V_j (M = 128, N = d, K = 128; P bf16 in TMEM, over S)
+// with c = scale log2 e. m is raised only when a row's maximum passed it by more
+// than 8 in the exponent: P stays below 2^8, which costs no accuracy in bf16 or
+// float32, and O is rescaled a few times per item instead of once per block.
+// Statistics, sums and O are float32; P is rounded to bf16 for the product (the
+// tensor cores take no wider A with a bf16 B), l adds the unrounded P.
+//
+// Roles: warps 0-3 own the rows of tile 0 (thread = row = TMEM lane), warps 4-7
+// those of tile 1, warp 8 loads (TMA), warp 9 issues the MMAs. The tensor cores
+// run S and P V of one tile while the other tile's warps form its softmax.
+// Every wait is bounded; the kernel drains its copies and MMAs before it ends.
+#include <string.h>
+
+#include "prompt.cuh"
+#include "tc_util.cuh"
+
+namespace sla {
+
+using namespace tc;
+
+struct PromptMaps {
+  CUtensorMap q, k, v;
+};
+
+struct PromptDev {
+  unsigned char* plan_dev;
+  const PromptItem* items;
+  const PromptJoin* joins;
+  __nv_bfloat16* o;
+  long long o_row, o_head;
+  float *lse, *part, *part_lse;
+  int Hq, G, tpt, causal, tiles;
+  long long Tq, Tk;
+  float scale, scale_log2;
+};
+
+namespace {
+
+constexpr int kThreads = 320;
+
+// D[tmem] (+)= A[tmem] * B[smem], warp-collective like mma_bf16
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                            uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                            int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+// 32 lanes x 32 columns of packed bf16 pairs
+__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+template <int D>
+struct FwdCfg {
+  static constexpr int kSub = 128 * 128;             // 128 rows x 128 bytes (64 columns)
+  static constexpr int kTileBytes = kSub * (D / 64);  // 128 x D bf16
+  static constexpr int kStages = D == 128 ? 4 : 8;   // K and V tiles in the ring
+  static constexpr int oQ = 0;
+  static constexpr int oKV = 2 * kTileBytes;
+  static constexpr int kBytes = oKV + kStages * kTileBytes;
+  static constexpr int kSmem = kBytes + 1024;
+  static constexpr int cO = 256;  // TMEM: S0 S1 (128 columns each), then O0 O1 (D each)
+};
+
+enum { bQ0 = 0, bQ1, bS0, bS1, bP0, bP1, bO0, bO1, bDone, bKV };  // then full / empty of every stage
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_fwd_kernel(const __grid_constant__ PromptMaps maps, const PromptDev a) {
+  using C = FwdCfg<D>;
+  constexpr int ST = C::kStages;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t bars[bKV + 2 * ST];
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* status = reinterpret_cast<int*>(a.plan_dev);
+  const PromptItem it = a.items[blockIdx.x];
+  if (it.q0 < 0 || it.nq < 1 || it.k0 < 0 || it.lk < 0 || it.q0 + (long long)it.nq > a.Tq ||
+      it.k0 + (long long)it.lk > a.Tk || it.nq > a.tiles * a.tpt || it.b0 < 0 || it.head < 0) {
+    if (threadIdx.x == 0) atomicExch(status, kDevBadIndex);
+    return;
+  }
+  // key blocks of tile t: [b0, nb_t)
+  auto end_block = [&](int t) {
+    const int last = min(it.nq, (t + 1) * a.tpt) - 1;
+    if (last < t * a.tpt) return it.b0;
+    const long long keys = a.causal ? min((long long)it.lk, (long long)it.pos0 + last + 1) : it.lk;
+    return max(it.b0, min(it.b1, int((max(keys, 0LL) + 127) / 128)));
+  };
+  const int nb0 = end_block(0), nb1 = end_block(1), bmax = max(nb0, nb1), n = bmax - it.b0;
+
+  volatile int* abort_flag = &abort_sh;
+  auto bar = [&](int b) { return smem_u32(&bars[b]); };
+  auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity, abort_flag, status); };
+  auto wait_w = [&](int b, uint32_t parity) {
+    const bool ok = wait(b, parity);
+    __syncwarp();
+    return ok;
+  };
+  int no_abort = 0;
+  auto wait_drain = [&](int b, uint32_t parity) {
+    return mbar_wait(bar(b), parity, reinterpret_cast<volatile int*>(&no_abort), status);
+  };
+  const uint32_t sb = smem_u32(smem);
+
+  if (threadIdx.x == 0) {
+    abort_sh = 0;
+    for (int i = 0; i < bKV + 2 * ST; ++i) mbar_init(bar(i), i == bP0 || i == bP1 ? 128 : 1);
+    fence_barrier_init();
+  }
+  if (warp == 9) tmem_alloc(smem_u32(&tmem_base_sh), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = tmem_base_sh;
+  // ring position of K (2 s) and V (2 s + 1) of step s
+  auto full = [&](int i) { return bKV + i % ST; };
+  auto empty = [&](int i) { return bKV + ST + i % ST; };
+  auto phase = [&](int i) { return uint32_t(i / ST) & 1; };
+
+  if (warp == 8) {
+    if (lane == 0 && n > 0) {
+      const int rows = a.G * a.tpt;
+      for (int t = 0; t < 2; ++t) {
+        if ((t == 0 ? nb0 : nb1) <= it.b0) continue;
+        mbar_expect_tx(bar(bQ0 + t), rows * D * 2);
+        for (int s = 0; s < D / 64; ++s)
+          tma_load_4d(sb + C::oQ + t * C::kTileBytes + s * C::kSub, &maps.q, bar(bQ0 + t), s * 64, 0,
+                      it.q0 + t * a.tpt, it.head);
+      }
+      int issued = 0;
+      for (int i = 0; i < 2 * n; ++i) {
+        if (!wait(empty(i), phase(i) ^ 1)) break;
+        issued = i + 1;
+        const int b = bmax - 1 - i / 2;
+        const CUtensorMap* m = (i & 1) ? &maps.v : &maps.k;
+        mbar_expect_tx(bar(full(i)), C::kTileBytes);
+        for (int s = 0; s < D / 64; ++s)
+          tma_load_3d(sb + C::oKV + (i % ST) * C::kTileBytes + s * C::kSub, m, bar(full(i)), s * 64,
+                      it.k0 + b * 128, it.head);
+      }
+      // every copy has landed before the CTA can end
+      if (nb0 > it.b0) wait_drain(bQ0, 0);
+      if (nb1 > it.b0) wait_drain(bQ1, 0);
+      for (int i = max(0, issued - ST); i < issued; ++i) wait_drain(full(i), phase(i));
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
+    constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
+    const int off[2] = {bmax - nb0, bmax - nb1};  // first step of each tile (n: none)
+    auto issue_s = [&](int t, int s) {
+      if (s == off[t]) wait_w(bQ0 + t, 0);
+      const uint32_t sq = sb + C::oQ + t * C::kTileBytes, sk = sb + C::oKV + ((2 * s) % ST) * C::kTileBytes;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t o = (k >> 2) * C::kSub + (k & 3) * 32;
+        mma_bf16(tb + t * 128, sdesc(sq + o, 16, 1024), sdesc(sk + o, 16, 1024), idS, k > 0);
+      }
+      mma_commit(bar(bS0 + t));
+    };
+    if (n > 0) {
+      wait_w(full(0), phase(0));
+      tc_fence_after();
+      for (int t = 0; t < 2; ++t)
+        if (off[t] == 0) issue_s(t, 0);
+      mma_commit(bar(empty(0)));
+    }
+    for (int s = 0; s < n; ++s) {
+      const int iv = 2 * s + 1;
+      const uint32_t sv = sb + C::oKV + (iv % ST) * C::kTileBytes;
+      wait_w(full(iv), phase(iv));
+      const int valid = it.lk - (bmax - 1 - s) * 128;
+      if (valid < 128) {
+        // the sequence ends inside this block: the rows behind it are another sequence's (0 x NaN is NaN)
+        for (int x = valid * 8 + lane; x < 128 * 8; x += 32)
+#pragma unroll
+          for (int sub = 0; sub < D / 64; ++sub)
+            *reinterpret_cast<uint4*>(smem + C::oKV + (iv % ST) * C::kTileBytes + sub * C::kSub + x * 16) =
+                make_uint4(0, 0, 0, 0);
+        fence_async_smem();
+        __syncwarp();
+      }
+      bool have_k = false;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (s >= off[t]) {
+          const int i = s - off[t];
+          wait_w(bP0 + t, i & 1);
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_bf16_ts(tb + C::cO + t * D, tb + t * 128 + k * 8, sdesc(sv + k * 2048, C::kSub, 1024), idO,
+                        (i > 0 || k > 0) ? 1u : 0u);
+          mma_commit(bar(bO0 + t));
+        }
+        if (s + 1 < n && s + 1 >= off[t]) {
+          if (!have_k) wait_w(full(2 * s + 2), phase(2 * s + 2));
+          have_k = true;
+          tc_fence_after();
+          issue_s(t, s + 1);
+        }
+      }
+      mma_commit(bar(empty(iv)));
+      if (s + 1 < n) mma_commit(bar(empty(2 * s + 2)));
+    }
+    mma_commit(bar(bDone));
+    wait_drain(bDone, 0);
+    __syncwarp();
+  } else {
+    const int t = warp >> 2, r = threadIdx.x & 127;
+    const int nb = t == 0 ? nb0 : nb1, steps = nb - it.b0;
+    const int tok = t * a.tpt + r / a.G, g = r - (r / a.G) * a.G;
+    const bool live = r < a.G * a.tpt && tok < it.nq;
+    // keys 0 .. limit - 1 are seen
+    const int limit = !live ? 0 : a.causal ? int(max(0LL, min((long long)it.lk, (long long)it.pos0 + tok + 1))) : it.lk;
+    const int warp_limit = __reduce_min_sync(0xffffffffu, limit);
+    const uint32_t tq = tb + (uint32_t(32 * (warp & 3)) << 16);
+    const uint32_t tS = tq + t * 128, tO = tq + C::cO + t * D;
+    const float c = a.scale_log2;
+    const float slack = 8.0f / c;
+    float m = -INFINITY, l = 0.0f;
+    for (int i = 0; i < steps; ++i) {
+      const int key0 = (nb - 1 - i) * 128;
+      wait_w(bS0 + t, i & 1);
+      tc_fence_after();
+      float s[128];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) tmem_ld32(tS + 32 * j, *reinterpret_cast<float(*)[32]>(&s[32 * j]));
+      tmem_wait_ld();
+      if (key0 + 128 > warp_limit) {
+        const int seen = limit - key0;
+#pragma unroll
+        for (int j = 0; j < 128; ++j) s[j] = j < seen ? s[j] : -INFINITY;
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int j = 4; j < 128; ++j) mx[j & 3] = max_nan(mx[j & 3], s[j]);
+      const float top = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3]));
+      const bool raise = !(top <= m + slack);  // NaN raises: the row becomes NaN
+      if (__any_sync(0xffffffffu, raise)) {
+        const float f = raise && m != -INFINITY ? ex2((m - top) * c) : 1.0f;
+        if (raise) m = top;
+        l *= f;
+        if (i > 0) {
+          wait_w(bO0 + t, (i - 1) & 1);  // P V of the block before has been added
+          tc_fence_after();
+#pragma unroll 1
+          for (int j = 0; j < D; j += 32) {
+            float o[32];
+            tmem_ld32(tO + j, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] *= f;
+            tmem_st32(tO + j, o);
+          }
+          tmem_wait_st();
+        }
+      }
+      const float mc = m == -INFINITY ? 0.0f : -m * c;
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      uint32_t p[64];
+#pragma unroll
+      for (int j = 0; j < 128; j += 2) {
+        const float x = ex2(fmaf(s[j], c, mc)), y = ex2(fmaf(s[j + 1], c, mc));
+        sum[(j >> 1) & 3] += x + y;
+        p[j >> 1] = pack_bf16(x, y);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st32u(tS, p);
+      tmem_st32u(tS + 32, p + 32);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar(bP0 + t));
+    }
+    if (steps > 0) {
+      wait_w(bO0 + t, (steps - 1) & 1);
+      tc_fence_after();
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const long long token = (long long)it.q0 + tok;
+    const int head = it.head * a.G + g;
+    const size_t prow = size_t(max(it.slot, 0)) * (a.tiles * 128) + (t * 128 + r);
+    __nv_bfloat16* orow = a.o + token * a.o_row + head * a.o_head;
+    float* part = a.part + prow * D;
+#pragma unroll 1
+    for (int j = 0; j < D; j += 32) {
+      float o[32];
+      if (steps > 0) {
+        tmem_ld32(tO + j, o);
+        tmem_wait_ld();
+      }
+#pragma unroll
+      for (int x = 0; x < 32; ++x) o[x] = l == 0.0f ? 0.0f : o[x] * inv;
+      if (!live) continue;
+      if (it.slot < 0) {
+#pragma unroll
+        for (int x = 0; x < 32; x += 8)
+          *reinterpret_cast<uint4*>(orow + j + x) =
+              make_uint4(pack_bf16(o[x], o[x + 1]), pack_bf16(o[x + 2], o[x + 3]), pack_bf16(o[x + 4], o[x + 5]),
+                         pack_bf16(o[x + 6], o[x + 7]));
+      } else {
+#pragma unroll
+        for (int x = 0; x < 32; x += 4)
+          *reinterpret_cast<float4*>(part + j + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+      }
+    }
+    if (live) {
+      const float lse2 = l == 0.0f ? -INFINITY : m * c + log2f(l);
+      if (it.slot >= 0)
+        a.part_lse[prow] = lse2;
+      else if (a.lse)
+        a.lse[token * a.Hq + head] = lse2 * 0.6931471805599453f;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tb, 512);
+  }
+}
+
+// Joins the partial results of rows whose keys were split: with L_i the parts'
+// log2-sums and M their maximum, O = sum 2^(L_i - M) O_i / sum 2^(L_i - M).
+// One warp per row, the parts in a fixed order. Bound: reading the parts.
+template <int D>
+__global__ void __launch_bounds__(128) prompt_join_kernel(const PromptDev a) {
+  const PromptJoin jn = a.joins[blockIdx.x];
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int t = r >> 7, rr = r & 127;
+  const int tok = t * a.tpt + rr / a.G, g = rr - (rr / a.G) * a.G;
+  if (rr >= a.G * a.tpt || tok >= jn.nq) return;
+  const size_t rows = size_t(a.tiles) * 128;
+  float mx = -INFINITY;
+  for (int i = 0; i < jn.n; ++i) mx = max_nan(mx, a.part_lse[(jn.first + i) * rows + r]);
+  float o[D / 32], den = 0.0f;
+#pragma unroll
+  for (int x = 0; x < D / 32; ++x) o[x] = 0.0f;
+  if (mx != -INFINITY) {
+    for (int i = 0; i < jn.n; ++i) {
+      const size_t at = (jn.first + i) * rows + r;
+      const float w = exp2f(a.part_lse[at] - mx);
+      den += w;
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) o[x] += w * a.part[at * D + lane * (D / 32) + x];
+    }
+  }
+  const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+  const long long token = (long long)jn.q0 + tok;
+  const int head = jn.head * a.G + g;
+  __nv_bfloat16* orow = a.o + token * a.o_row + head * a.o_head + lane * (D / 32);
+#pragma unroll
+  for (int x = 0; x < D / 32; x += 2) *reinterpret_cast<uint32_t*>(orow + x) = pack_bf16(o[x] * inv, o[x + 1] * inv);
+  if (lane == 0 && a.lse)
+    a.lse[token * a.Hq + head] = den == 0.0f ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
+}
+
+namespace {
+
+// Packed query rows: (d, G, tokens, key heads), boxes of 64 values x G heads x tpt tokens.
+bool map_queries(CUtensorMap* m, const PromptTensor& t, int d, int G, int Hkv, long long T, int tpt) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(G), cuuint64_t(T), cuuint64_t(Hkv)};
+  cuuint64_t strides[3] = {cuuint64_t(t.head) * 2, cuuint64_t(t.row) * 2, cuuint64_t(t.head) * 2 * G};
+  cuuint32_t box[4] = {64, cuuint32_t(G), cuuint32_t(tpt), 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t.base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Keys or values: (d, tokens, key heads), boxes of 64 values x 128 tokens.
+bool map_keys(CUtensorMap* m, const PromptTensor& t, int d, int Hkv, long long T) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(T), cuuint64_t(Hkv)};
+  cuuint64_t strides[2] = {cuuint64_t(t.row) * 2, cuuint64_t(t.head) * 2};
+  cuuint32_t box[3] = {64, 128, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t.base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_d(const PromptArgs& a, const PromptMaps& maps, const PromptDev& v, cudaStream_t s) {
+  cudaError_t e =
+      cudaFuncSetAttribute(prompt_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdCfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  prompt_fwd_kernel<D><<<a.plan->n_items, kThreads, FwdCfg<D>::kSmem, s>>>(maps, v);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.plan->n_joins == 0) return e;
+  prompt_join_kernel<D><<<dim3(a.plan->n_joins, a.plan->tiles * 32), 128, 0, s>>>(v);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s) {
+  const PromptPlan& p = *a.plan;
+  PromptMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  PromptDev v{};
+  v.plan_dev = a.plan_dev;
+  v.items = reinterpret_cast<const PromptItem*>(a.plan_dev + p.items);
+  v.joins = reinterpret_cast<const PromptJoin*>(a.plan_dev + p.joins);
+  v.o = static_cast<__nv_bfloat16*>(a.o.base);
+  v.o_row = a.o.row;
+  v.o_head = a.o.head;
+  v.lse = a.lse;
+  v.part = a.part;
+  v.part_lse = a.part_lse;
+  v.Hq = p.Hq;
+  v.G = p.G;
+  v.tpt = kPromptTile / p.G;
+  v.causal = p.causal;
+  v.tiles = p.tiles;
+  v.Tq = p.Tq;
+  v.Tk = p.Tk;
+  v.scale = p.scale;
+  v.scale_log2 = p.scale * kLog2e;
+  if (!map_queries(&maps.q, a.q, p.d, p.G, p.Hkv, p.Tq, v.tpt)) return cudaErrorInvalidValue;
+  if (p.Tk > 0 && (!map_keys(&maps.k, a.k, p.d, p.Hkv, p.Tk) || !map_keys(&maps.v, a.v, p.d, p.Hkv, p.Tk)))
+    return cudaErrorInvalidValue;
+  return p.d == 128 ? launch_d<128>(a, maps, v, s) : launch_d<64>(a, maps, v, s);
+}
+
+}  // namespace sla

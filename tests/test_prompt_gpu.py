@@ -1,0 +1,229 @@
+"""Packed prompt attention on the GPU against float64."""
+
+import math
+
+import pytest
+import torch
+
+from tests import operator_reference as R
+
+pytestmark = pytest.mark.gpu
+
+H8 = 2.0 ** -8  # half a bf16 step, relative
+
+# lens_q, lens_k, Hq, Hkv, d, causal
+CASES = [
+    ([1], None, 1, 1, 64, True),
+    ([1], None, 4, 1, 128, False),
+    ([127, 1, 128, 129], None, 2, 2, 128, True),
+    ([300, 17], None, 3, 1, 64, True),         # groups of 3: 42 tokens to a tile, 2 rows idle
+    ([255, 513, 64], None, 4, 2, 128, True),
+    ([100, 260], None, 5, 1, 128, False),
+    ([33, 0, 65], None, 6, 3, 64, True),       # an empty sequence between two
+    ([40], None, 65, 1, 64, True),             # one token to a tile, almost half of it idle
+    ([9], None, 128, 1, 64, True),
+    ([1, 1, 1], [1, 700, 129], 8, 2, 128, True),     # single tokens over caches
+    ([1, 3], [5000, 4100], 4, 2, 128, True),         # long enough for split keys
+    ([1], [20000], 7, 1, 64, False),
+    ([50, 200], [450, 200], 4, 4, 64, True),         # a piece behind a cache
+    ([130, 7], [60, 0], 2, 1, 128, True),            # rows that see nothing
+    ([5], [0, ], 2, 1, 64, False),                   # no keys at all
+    ([5, 4], [0, 3], 2, 1, 64, False),
+    ([600], None, 2, 1, 128, True),
+]
+IDS = lambda c: f"{c[0]}-{c[1]}-{c[2]}x{c[3]}-{c[4]}-{'causal' if c[5] else 'full'}".replace(" ", "")  # noqa: E731
+
+
+def make(case, seed=0, spread=1.0):
+    lq, lk, Hq, Hkv, d, causal = case
+    lk = lq if lk is None else lk
+    g = torch.Generator().manual_seed(seed)
+    q = (torch.randn(sum(lq), Hq, d, generator=g) * spread).bfloat16()
+    k = torch.randn(sum(lk), Hkv, d, generator=g).bfloat16()
+    v = torch.randn(sum(lk), Hkv, d, generator=g).bfloat16()
+    do = torch.randn(sum(lq), Hq, d, generator=g).bfloat16()
+    return q, k, v, do, lq, lk
+
+
+def plan_of(sla, case, **kw):
+    lq, lk, Hq, Hkv, d, causal = case
+    return sla.prompt_plan(lq, lk, Hq=Hq, Hkv=Hkv, d=d, causal=causal, **kw)
+
+
+def score_error(d, q, k, scale):
+    """How far a score's exponent may be off: float32 sums of d products in any order (d half-steps of
+    the sum of their sizes, twice for truncating adders), the float32 exponent's own rounding and 2^x's."""
+    size = (q.abs().double().amax() * k.abs().double().amax() * d * scale).item() if k.numel() else 0.0
+    return (2 * d + 4) * R.EPS32 * size + 2.0 ** -21
+
+
+def check_forward(case, o, lse, ref, q, k, scale=None):
+    d = case[4]
+    e = score_error(d, q, k, 1 / math.sqrt(d) if scale is None else scale)
+    # P rounded to bf16, off by e in the exponent (twice: P and the sum), O rounded to bf16
+    bound = (H8 + 3 * e) * ref["o_size"] * 1.01 + H8 * ref["o"].abs() * 1.01 + 1e-30
+    err = (o.cpu().double() - ref["o"]).abs()
+    assert (err <= bound).all(), (err / bound).max()
+    if lse is not None:
+        got, want = lse.cpu().double(), ref["lse"]
+        assert torch.equal(got == -math.inf, want == -math.inf)
+        fin = want != -math.inf
+        assert ((got[fin] - want[fin]).abs() <= 2 * e + 2.0 ** -21 * (1 + want[fin].abs())).all()
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_forward(cuda_lib, case):
+    sla = cuda_lib
+    q, k, v, _, lq, lk = make(case)
+    plan = plan_of(sla, case)
+    o, lse = sla.prompt_forward(q.cuda(), k.cuda(), v.cuda(), plan)
+    assert sla.read_device_status(plan.device_bytes) == 0
+    check_forward(case, o, lse, R.prompt(q, k, v, lq, lk, case[5]), q, k)
+    assert torch.equal(sla.prompt_attention(q.cuda(), k.cuda(), v.cuda(), plan), o)  # bit for bit, again
+
+
+@pytest.mark.parametrize("case", [CASES[2], CASES[10], CASES[3]], ids=IDS)
+@pytest.mark.parametrize("spread,scale", [(30.0, None), (1.0, 1e-4), (0.0, 1.0)])
+def test_forward_of_peaked_and_flat_rows(cuda_lib, case, spread, scale):
+    sla = cuda_lib
+    q, k, v, _, lq, lk = make(case, seed=1, spread=spread)
+    plan = plan_of(sla, case, softmax_scale=scale or 0.0)
+    o, lse = sla.prompt_forward(q.cuda(), k.cuda(), v.cuda(), plan)
+    check_forward(case, o, lse, R.prompt(q, k, v, lq, lk, case[5], scale), q, k, scale)
+
+
+def test_growing_maxima(cuda_lib):
+    """Scores that grow towards the first keys: the running maximum is raised in every block."""
+    sla = cuda_lib
+    case = ([700], None, 2, 1, 128, True)
+    q, k, v, _, lq, lk = make(case, seed=2)
+    q[..., 0], k[:, :, 0] = 8.0, torch.linspace(120.0, 0.0, 700)[:, None].bfloat16()
+    o, lse = sla.prompt_forward(q.cuda(), k.cuda(), v.cuda(), plan_of(sla, case))
+    check_forward(case, o, lse, R.prompt(q, k, v, lq, lk, True), q, k)
+    case = ([700], None, 2, 1, 128, False)
+    o, lse = sla.prompt_forward(q.cuda(), k.cuda(), v.cuda(), plan_of(sla, case))
+    check_forward(case, o, lse, R.prompt(q, k, v, lq, lk, False), q, k)
+
+
+def test_strided_rows_and_rows_behind_the_last_sequence(cuda_lib):
+    sla = cuda_lib
+    case = ([70, 200, 33], None, 4, 2, 64, True)
+    q, k, v, _, lq, _ = make(case)
+    plan = plan_of(sla, case)
+    want = sla.prompt_attention(q.cuda(), k.cuda(), v.cuda(), plan)
+    # one projection's output with 41 more tokens of NaN behind the last sequence
+    x = torch.full((sum(lq) + 41, 4 + 2 + 2, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    x[:sum(lq), :4], x[:sum(lq), 4:6], x[:sum(lq), 6:] = q.cuda(), k.cuda(), v.cuda()
+    out = torch.full((sum(lq) + 41, 4, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    sla.prompt_forward(x[:, :4], x[:, 4:6], x[:, 6:], plan, out=out)
+    assert torch.equal(out[:sum(lq)], want) and (out[sum(lq):] == 5.0).all()
+    # head-major memory, rows that are not 16-byte steps apart, a broadcast head
+    hm = [t.cuda().transpose(0, 1).contiguous().transpose(0, 1) for t in (q, k, v)]
+    assert torch.equal(sla.prompt_attention(*hm, plan), want)
+    odd = torch.zeros(sum(lq), 4, 67, dtype=torch.bfloat16, device="cuda")
+    odd[..., 1:65] = q.cuda()
+    assert torch.equal(sla.prompt_attention(odd[..., 1:65], k.cuda(), v.cuda(), plan), want)
+    ke, ve = (t.cuda()[:, :1].expand(-1, 2, -1) for t in (k, v))
+    assert torch.equal(sla.prompt_attention(q.cuda(), ke, ve, plan),
+                       sla.prompt_attention(q.cuda(), ke.contiguous(), ve.contiguous(), plan))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_sequences_do_not_touch_each_other(cuda_lib, d):
+    """NaN and infinities in one sequence stay in it."""
+    sla = cuda_lib
+    case = ([70, 150, 33], None, 3, 1, d, True)
+    q, k, v, _, lq, _ = make(case, seed=3)
+    plan = plan_of(sla, case)
+    want = sla.prompt_attention(q.cuda(), k.cuda(), v.cuda(), plan)
+    for bad in (float("nan"), float("inf")):
+        ts = [t.clone() for t in (q, k, v)]
+        for t in ts:
+            t[70:220] = bad
+        got = sla.prompt_attention(*(t.cuda() for t in ts), plan)
+        keep = torch.ones(253, dtype=torch.bool)
+        keep[70:220] = False
+        assert torch.equal(got[keep], want[keep])
+        assert not torch.isfinite(got[70:220].float()).any()
+
+
+def test_future_keys_do_not_reach_the_past(cuda_lib):
+    sla = cuda_lib
+    case = ([500], None, 2, 1, 128, True)
+    q, k, v, _, _, _ = make(case, seed=4)
+    plan = plan_of(sla, case)
+    want = sla.prompt_attention(q.cuda(), k.cuda(), v.cuda(), plan)
+    k2, v2 = k.clone(), v.clone()
+    k2[300:], v2[300:] = 100.0, -77.0
+    got = sla.prompt_attention(q.cuda(), k2.cuda(), v2.cuda(), plan)
+    assert torch.equal(got[:300], want[:300]) and not torch.equal(got[300:], want[300:])
+    k2[300:] = float("nan")  # a score that the mask leaves out may be anything
+    got = sla.prompt_attention(q.cuda(), k2.cuda(), v.cuda(), plan)
+    assert torch.equal(got[:300], want[:300]) and torch.isnan(got[300:].float()).all()
+
+
+def test_a_prompt_in_pieces_is_the_whole_prompt(cuda_lib):
+    """Pieces and single tokens over the cache give the whole prompt's rows."""
+    sla = cuda_lib
+    case = ([260], None, 4, 2, 128, True)
+    q, k, v, _, _, _ = make(case, seed=5)
+    ref = R.prompt(q, k, v, [260], [260], True)
+    q, k, v = q.cuda(), k.cuda(), v.cuda()
+    for a, b in ((0, 100), (100, 230), (230, 259), (259, 260)):
+        plan = sla.prompt_plan([b - a], [b], Hq=4, Hkv=2, d=128)
+        o, lse = sla.prompt_forward(q[a:b], k[:b], v[:b], plan)
+        part = {n: t[a:b] for n, t in ref.items()}
+        check_forward(case, o, lse, part, q.cpu(), k.cpu())
+
+
+def test_streams_graphs_and_two_calls_of_one_plan(cuda_lib):
+    sla = cuda_lib
+    case = ([1, 2], [9000, 6000], 8, 2, 128, True)  # split keys: the calls have workspaces
+    q, k, v, _, _, _ = make(case, seed=6)
+    q, k, v = q.cuda(), k.cuda(), v.cuda()
+    plan = plan_of(sla, case)
+    assert plan._workspace > 0
+    want, want_lse = sla.prompt_forward(q, k, v, plan)
+    q2 = q.flip(1).contiguous()
+    want2, _ = sla.prompt_forward(q2, k, v, plan)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        a, _ = sla.prompt_forward(q, k, v, plan, stream=side)
+        b, _ = sla.prompt_forward(q2, k, v, plan)
+    torch.cuda.synchronize()
+    assert torch.equal(a, want) and torch.equal(b, want2)
+    graphs = []
+    for x in (q, q2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = sla.prompt_forward(x, k, v, plan)
+        graphs.append((g, y))
+    for _ in range(3):
+        for g, y in graphs:
+            y[0].zero_()
+            g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(graphs[0][1][0], want) and torch.equal(graphs[0][1][1], want_lse)
+    assert torch.equal(graphs[1][1][0], want2)
+    assert sla.read_device_status(plan.device_bytes) == 0
+
+
+def test_refusals(cuda_lib):
+    sla = cuda_lib
+    case = ([10, 20], None, 4, 2, 64, True)
+    q, k, v, _, _, _ = make(case)
+    q, k, v = q.cuda(), k.cuda(), v.cuda()
+    plan = plan_of(sla, case)
+    for bad in ((q[:29], k, v), (q, k[:29], v), (q[:, :3], k, v), (q, k, v[:, :1]), (q[..., :32], k, v),
+                (q.float(), k, v), (q, k.half(), v), (q.cpu(), k, v), (q[0], k, v)):
+        with pytest.raises(ValueError):
+            sla.prompt_attention(*bad, plan)
+    with pytest.raises(ValueError):
+        sla.prompt_forward(q, k, v, plan, out=torch.empty(30, 4, 64, device="cuda"))
+    with pytest.raises(sla.SLAError):
+        sla.prompt_forward(q, k, v, plan, out=torch.empty(1, 4, 64, device="cuda", dtype=torch.bfloat16).expand(30, 4, 64))
+    small = sla.prompt_plan([1], [9000], Hq=4, Hkv=2, d=64)
+    kk = torch.zeros(9000, 2, 64, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(sla.SLAError):
+        sla.prompt_forward(q[:1], kk, kk, small, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
