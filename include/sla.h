@@ -423,6 +423,7 @@ typedef struct sla_prompt_params {
   int Hq, Hkv;           /* Hq a multiple of Hkv, Hq / Hkv <= 128 */
   int d;                 /* 64 or 128 */
   int causal;            /* 0 or 1 */
+  int backward;          /* 1: the plan also lists sla_prompt_backward's items */
   float softmax_scale;   /* 0 selects 1/sqrt(d) */
 } sla_prompt_params;
 
@@ -447,6 +448,17 @@ size_t sla_prompt_workspace_size(const void* plan);
 sla_status sla_prompt_forward(const sla_rows* q, const sla_rows* k, const sla_rows* v, const sla_rows* o, float* lse,
                               const void* plan, size_t plan_bytes, void* plan_device, void* workspace,
                               size_t workspace_bytes, void* stream);
+
+/* Gradients of <dO, O> for a forward of the same plan, which must have been made
+ * with backward = 1 (SLA_ERR_UNSUPPORTED otherwise).
+ *   q, k, v, o, lse  the forward's inputs and results.
+ *   dq, dk, dv       outputs; a key head's dk, dv add up its group's query heads.
+ * Deterministic. Rows behind the last sequence are neither read nor written. */
+size_t sla_prompt_backward_workspace_size(const void* plan);
+sla_status sla_prompt_backward(const sla_rows* q, const sla_rows* k, const sla_rows* v, const sla_rows* o,
+                               const float* lse, const sla_rows* dO, const sla_rows* dq, const sla_rows* dk,
+                               const sla_rows* dv, const void* plan, size_t plan_bytes, void* plan_device,
+                               void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

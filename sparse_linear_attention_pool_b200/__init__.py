@@ -42,7 +42,7 @@ EXPORTS = ("sla_abi_version", "sla_status_string", "sla_validate", "sla_workspac
            "sla_backward", "sla_check_wait_timeout",
            "sla_rope", "sla_qk_norm_rope", "sla_qk_norm_rope_backward_workspace_size", "sla_qk_norm_rope_backward",
            "sla_prompt_validate", "sla_prompt_plan_size", "sla_prompt_plan", "sla_prompt_workspace_size",
-           "sla_prompt_forward")
+           "sla_prompt_forward", "sla_prompt_backward_workspace_size", "sla_prompt_backward")
 NOALLOC_WORKSPACE_BYTES = 32 << 20
 NUM_STAGES = 6
 STAGES = ("pool", "phik_hz", "scores", "classify", "hz_reduce", "attention")
@@ -86,7 +86,7 @@ class PromptParams(ctypes.Structure):
     """Mirror of struct sla_prompt_params (len_q, len_k: host addresses)."""
     _fields_ = [("n_seq", ctypes.c_int), ("len_q", ctypes.c_void_p), ("len_k", ctypes.c_void_p),
                 ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("causal", ctypes.c_int),
-                ("softmax_scale", ctypes.c_float)]
+                ("backward", ctypes.c_int), ("softmax_scale", ctypes.c_float)]
 
 
 class Rows(ctypes.Structure):
@@ -141,6 +141,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sla_prompt_plan": (i, [PP, vp, sz]),
         "sla_prompt_workspace_size": (sz, [vp]),
         "sla_prompt_forward": (i, [TP, TP, TP, TP, vp, vp, sz, vp, vp, sz, vp]),
+        "sla_prompt_backward_workspace_size": (sz, [vp]),
+        "sla_prompt_backward": (i, [TP, TP, TP, TP, vp, TP, TP, TP, TP, vp, sz, vp, vp, sz, vp]),
         "sla_stage_timing": (i, [i]),
         "sla_stage_times": (i, [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int)]),
     }
@@ -434,5 +436,5 @@ def attention(q, k, v, *, N: Optional[int] = None, variant: str = "sla", k_crit:
     return _SLAFunction.apply(q, k, v, w_proj, alpha)
 
 
-from .prompt import PromptPlan, prompt_attention, prompt_forward, prompt_plan  # noqa: E402,F401
+from .prompt import PromptPlan, prompt_attention, prompt_backward, prompt_forward, prompt_plan  # noqa: E402,F401
 from .rope import RopeTable, qk_norm_rope, qk_norm_rope_backward, rope, rope_table  # noqa: E402,F401

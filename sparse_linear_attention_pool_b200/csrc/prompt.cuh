@@ -32,6 +32,13 @@ struct PromptKeys {
   int block;     // key block
   int head;
   int t0, t1;
+  int slot;      // < 0: writes dK and dV itself; else the slot of its partial sums
+  int pad[3];
+};
+// A key tile whose query tiles were split: slots first .. first + n - 1 are added.
+struct PromptKeysJoin {
+  int row, nk;   // first key row, keys
+  int head, first, n, pad[3];
 };
 
 struct PromptPlan {
@@ -41,12 +48,13 @@ struct PromptPlan {
   float scale;
   int tiles;   // query tiles per forward item (1 or 2)
   long long Tq, Tk;
-  int n_items, n_joins, n_slots, n_keys, n_rows;  // n_rows: dQ items
-  unsigned long long items, joins, keys, rows, total;  // byte offsets
+  int n_items, n_joins, n_slots;
+  // backward (all 0 in a plan without it)
+  int n_keys, n_kjoins, n_kslots, n_rows, row_tiles;  // n_rows: dQ items, of row_tiles query tiles each
+  unsigned long long items, joins, keys, kjoins, rows, total;  // byte offsets
 };
 constexpr unsigned kPromptMagic = 0x534c4131u;
 
-struct PromptMaps;
 struct PromptTensor {
   void* base;
   long long row, head;
@@ -60,6 +68,15 @@ struct PromptArgs {
   float* part;                // [slots][tiles 128][d] partial O
   float* part_lse;            // [slots][tiles 128], log2
 };
+struct PromptGradArgs {
+  const PromptPlan* plan;
+  unsigned char* plan_dev;
+  PromptTensor q, k, v, o, dO, dq, dk, dv;
+  const float* lse;   // [Tq, Hq]
+  float2* ld;         // [Hkv][Tq G]: (lse log2 e, rowsum dO O)
+  float* part;        // [key slots][2][128][d] partial dK, dV
+};
+cudaError_t launch_prompt_backward(const PromptGradArgs& a, cudaStream_t s);
 cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s);
 
 }  // namespace sla

@@ -21,7 +21,7 @@ namespace {
 sla_status check_params(const sla_prompt_params* p) {
   if (p == nullptr || p->n_seq < 1 || p->len_q == nullptr) return SLA_ERR_INVALID_ARG;
   if (p->Hq < 1 || p->Hkv < 1 || p->Hq % p->Hkv != 0) return SLA_ERR_INVALID_ARG;
-  if (p->causal != 0 && p->causal != 1) return SLA_ERR_INVALID_ARG;
+  if ((p->causal != 0 && p->causal != 1) || (p->backward != 0 && p->backward != 1)) return SLA_ERR_INVALID_ARG;
   if (!(p->softmax_scale >= 0.0f) || isinf(p->softmax_scale)) return SLA_ERR_INVALID_ARG;
   if (p->d != 64 && p->d != 128) return SLA_ERR_UNSUPPORTED;
   if (p->Hq / p->Hkv > 128 || p->Hq > 65535) return SLA_ERR_UNSUPPORTED;
@@ -42,7 +42,8 @@ struct Lists {
   std::vector<PromptItem> items, rows;
   std::vector<PromptJoin> joins;
   std::vector<PromptKeys> keys;
-  int tiles = 2, slots = 0;
+  std::vector<PromptKeysJoin> kjoins;
+  int tiles = 2, slots = 0, row_tiles = 2, kslots = 0;
 };
 
 int key_blocks(const sla_prompt_params& p, int lq, int lk, int last_token) {
@@ -109,6 +110,8 @@ double split_cost(const std::vector<PromptItem>& items, int chunk, double step) 
   return makespan(cost) + (any ? kJoinCost : 0.0);
 }
 
+void add_backward(const sla_prompt_params& p, Lists& L);
+
 Lists make_lists(const sla_prompt_params& p) {
   Lists L;
   const int G = p.Hq / p.Hkv, tpt = kPromptTile / G;
@@ -156,7 +159,91 @@ Lists make_lists(const sla_prompt_params& p) {
   }
   auto longer = [](const PromptItem& a, const PromptItem& b) { return a.b1 - a.b0 > b.b1 - b.b0; };
   std::stable_sort(L.items.begin(), L.items.end(), longer);
+  if (p.backward) add_backward(p, L);
   return L;
+}
+
+// Backward: dQ items like the forward's, and one item per key tile, whose query
+// tiles are split where few key tiles see many of them.
+void add_backward(const sla_prompt_params& p, Lists& L) {
+  const int G = p.Hq / p.Hkv, tpt = kPromptTile / G;
+  auto longer = [](const PromptItem& a, const PromptItem& b) { return a.b1 > b.b1; };
+  double best = 0.0;
+  for (int tiles = 2; tiles >= 1; --tiles) {
+    std::vector<PromptItem> rows = row_items(p, tiles * tpt);
+    if (tiles == 1 && rows.size() >= 8 * kPromptSms) break;
+    const double c = split_cost(rows, 0, tiles == 2 ? 1.0 : kOneTile);
+    if (tiles == 2 || c < best) {
+      best = c;
+      L.rows = std::move(rows);
+      L.row_tiles = tiles;
+    }
+  }
+  std::stable_sort(L.rows.begin(), L.rows.end(), longer);
+
+  std::vector<PromptKeys> base;
+  int q0 = 0, k0 = 0;
+  long long total = 0;
+  for (int s = 0; s < p.n_seq; ++s) {
+    const int lq = p.len_q[s], lk = p.len_k ? p.len_k[s] : lq;
+    const int tiles = (lq + tpt - 1) / tpt;
+    for (int b = 0; b < (lk + kPromptTile - 1) / kPromptTile; ++b)
+      for (int h = 0; h < p.Hkv; ++h) {
+        // the first query that sees the block's first key
+        const long long first = p.causal ? std::max(0LL, (long long)b * kPromptTile - (lk - lq)) : 0;
+        PromptKeys it{};
+        it.k0 = k0;
+        it.lk = lk;
+        it.q0 = q0;
+        it.lq = lq;
+        it.block = b;
+        it.head = h;
+        it.t0 = int(std::min<long long>(tiles, first / tpt));
+        it.t1 = tiles;
+        it.slot = -1;
+        total += it.t1 - it.t0;
+        base.push_back(it);
+      }
+    q0 += lq;
+    k0 += lk;
+  }
+  std::vector<int> chunks = {0};
+  if (base.size() < 4 * kPromptSms)
+    for (int w : {1, 2, 3}) chunks.push_back(int(std::max(4LL, total / (kPromptSms * w) + 1)));
+  int chunk = 0;
+  best = -1.0;
+  for (int c : chunks) {
+    std::vector<double> cost;
+    bool any = false;
+    for (const PromptKeys& it : base) {
+      const int n = pieces(it.t1 - it.t0, c);
+      any = any || n > 1;
+      for (int i = 0; i < n; ++i) cost.push_back(kItemCost + double((it.t1 - it.t0 + n - 1) / n));
+    }
+    const double m = makespan(cost) + (any ? kJoinCost : 0.0);
+    if (best < 0.0 || m < best) {
+      best = m;
+      chunk = c;
+    }
+  }
+  for (const PromptKeys& it : base) {
+    const int len = it.t1 - it.t0, n = pieces(len, chunk);
+    if (n == 1) {
+      L.keys.push_back(it);
+      continue;
+    }
+    L.kjoins.push_back(PromptKeysJoin{it.k0 + it.block * kPromptTile, std::min(kPromptTile, it.lk - it.block * kPromptTile),
+                                      it.head, L.kslots, n, {}});
+    for (int i = 0; i < n; ++i) {
+      PromptKeys part = it;
+      part.t0 = it.t0 + int((long long)len * i / n);
+      part.t1 = it.t0 + int((long long)len * (i + 1) / n);
+      part.slot = L.kslots++;
+      L.keys.push_back(part);
+    }
+  }
+  std::stable_sort(L.keys.begin(), L.keys.end(),
+                   [](const PromptKeys& a, const PromptKeys& b) { return a.t1 - a.t0 > b.t1 - b.t0; });
 }
 
 size_t layout(const sla_prompt_params& p, const Lists& L, PromptPlan* h) {
@@ -178,7 +265,10 @@ size_t layout(const sla_prompt_params& p, const Lists& L, PromptPlan* h) {
   h->n_joins = int(L.joins.size());
   h->n_slots = L.slots;
   h->n_keys = int(L.keys.size());
+  h->n_kjoins = int(L.kjoins.size());
+  h->n_kslots = L.kslots;
   h->n_rows = int(L.rows.size());
+  h->row_tiles = L.row_tiles;
   size_t off = align256(sizeof(PromptPlan));
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -188,6 +278,7 @@ size_t layout(const sla_prompt_params& p, const Lists& L, PromptPlan* h) {
   h->items = take(L.items.size() * sizeof(PromptItem));
   h->joins = take(L.joins.size() * sizeof(PromptJoin));
   h->keys = take(L.keys.size() * sizeof(PromptKeys));
+  h->kjoins = take(L.kjoins.size() * sizeof(PromptKeysJoin));
   h->rows = take(L.rows.size() * sizeof(PromptItem));
   h->total = off;
   return off;
@@ -219,6 +310,10 @@ sla_status check_rows(const sla_rows* t, long long T, int H, int d, bool output,
 
 size_t forward_workspace(const PromptPlan& p) {
   return p.n_slots == 0 ? 0 : align256(size_t(p.n_slots) * p.tiles * 128 * (size_t(p.d) + 1) * sizeof(float));
+}
+
+size_t backward_workspace(const PromptPlan& p) {
+  return align256(size_t(p.Tq) * p.Hq * sizeof(float2)) + size_t(p.n_kslots) * 2 * 128 * p.d * sizeof(float);
 }
 
 sla_status check_workspace(const void* ws, size_t have, size_t need) {
@@ -255,6 +350,7 @@ sla_status sla_prompt_plan(const sla_prompt_params* p, void* plan, size_t plan_b
   put(h.items, L.items.data(), L.items.size() * sizeof(PromptItem));
   put(h.joins, L.joins.data(), L.joins.size() * sizeof(PromptJoin));
   put(h.keys, L.keys.data(), L.keys.size() * sizeof(PromptKeys));
+  put(h.kjoins, L.kjoins.data(), L.kjoins.size() * sizeof(PromptKeysJoin));
   put(h.rows, L.rows.data(), L.rows.size() * sizeof(PromptItem));
   return SLA_OK;
 }
@@ -284,6 +380,42 @@ sla_status sla_prompt_forward(const sla_rows* q, const sla_rows* k, const sla_ro
   a.part = static_cast<float*>(workspace);
   a.part_lse = a.part + size_t(p->n_slots) * p->tiles * 128 * p->d;
   return launch_prompt_forward(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SLA_OK : SLA_ERR_CUDA;
+}
+
+size_t sla_prompt_backward_workspace_size(const void* plan) {
+  const PromptPlan* p = plan_of(plan, ~size_t(0));
+  return p == nullptr || p->n_rows == 0 ? 0 : backward_workspace(*p);
+}
+
+sla_status sla_prompt_backward(const sla_rows* q, const sla_rows* k, const sla_rows* v, const sla_rows* o,
+                               const float* lse, const sla_rows* dO, const sla_rows* dq, const sla_rows* dk,
+                               const sla_rows* dv, const void* plan, size_t plan_bytes, void* plan_device,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  const PromptPlan* p = plan_of(plan, plan_bytes);
+  if (p == nullptr || plan_device == nullptr || lse == nullptr) return SLA_ERR_INVALID_ARG;
+  if (p->n_rows == 0) return SLA_ERR_UNSUPPORTED;  // planned without the backward
+  PromptGradArgs a{};
+  sla_status st = check_rows(q, p->Tq, p->Hq, p->d, false, &a.q);
+  if (st == SLA_OK) st = check_rows(o, p->Tq, p->Hq, p->d, false, &a.o);
+  if (st == SLA_OK) st = check_rows(dO, p->Tq, p->Hq, p->d, false, &a.dO);
+  if (st == SLA_OK) st = check_rows(dq, p->Tq, p->Hq, p->d, true, &a.dq);
+  if (p->Tk > 0) {
+    if (st == SLA_OK) st = check_rows(k, p->Tk, p->Hkv, p->d, false, &a.k);
+    if (st == SLA_OK) st = check_rows(v, p->Tk, p->Hkv, p->d, false, &a.v);
+    if (st == SLA_OK) st = check_rows(dk, p->Tk, p->Hkv, p->d, true, &a.dk);
+    if (st == SLA_OK) st = check_rows(dv, p->Tk, p->Hkv, p->d, true, &a.dv);
+  }
+  if (st != SLA_OK) return st;
+  if (!aligned(plan_device, 256) || !aligned(lse, 4)) return SLA_ERR_ALIGNMENT;
+  st = check_workspace(workspace, workspace_bytes, backward_workspace(*p));
+  if (st != SLA_OK) return st;
+  a.plan = p;
+  a.plan_dev = static_cast<unsigned char*>(plan_device);
+  a.lse = lse;
+  a.ld = static_cast<float2*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
+                                    align256(size_t(p->Tq) * p->Hq * sizeof(float2)));
+  return launch_prompt_backward(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SLA_OK : SLA_ERR_CUDA;
 }
 
 }  // extern "C"

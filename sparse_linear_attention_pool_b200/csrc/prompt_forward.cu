@@ -18,8 +18,7 @@
 // Every wait is bounded; the kernel drains its copies and MMAs before it ends.
 #include <string.h>
 
-#include "prompt.cuh"
-#include "tc_util.cuh"
+#include "prompt_tc.cuh"
 
 namespace sla {
 
@@ -44,40 +43,6 @@ struct PromptDev {
 namespace {
 
 constexpr int kThreads = 320;
-
-// D[tmem] (+)= A[tmem] * B[smem], warp-collective like mma_bf16
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                            uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
-}
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
-                                            int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
-      "%4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
-      : "memory");
-}
-// 32 lanes x 32 columns of packed bf16 pairs
-__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
 
 template <int D>
 struct FwdCfg {
@@ -392,38 +357,15 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const PromptDev a) {
 
 namespace {
 
-// Packed query rows: (d, G, tokens, key heads), boxes of 64 values x G heads x tpt tokens.
-bool map_queries(CUtensorMap* m, const PromptTensor& t, int d, int G, int Hkv, long long T, int tpt) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(G), cuuint64_t(T), cuuint64_t(Hkv)};
-  cuuint64_t strides[3] = {cuuint64_t(t.head) * 2, cuuint64_t(t.row) * 2, cuuint64_t(t.head) * 2 * G};
-  cuuint32_t box[4] = {64, cuuint32_t(G), cuuint32_t(tpt), 1};
-  cuuint32_t es[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t.base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-// Keys or values: (d, tokens, key heads), boxes of 64 values x 128 tokens.
-bool map_keys(CUtensorMap* m, const PromptTensor& t, int d, int Hkv, long long T) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(T), cuuint64_t(Hkv)};
-  cuuint64_t strides[2] = {cuuint64_t(t.row) * 2, cuuint64_t(t.head) * 2};
-  cuuint32_t box[3] = {64, 128, 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t.base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+template <int D>
+cudaError_t set_up() {
+  return cudaFuncSetAttribute(prompt_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdCfg<D>::kSmem);
 }
 
 template <int D>
 cudaError_t launch_d(const PromptArgs& a, const PromptMaps& maps, const PromptDev& v, cudaStream_t s) {
-  cudaError_t e =
-      cudaFuncSetAttribute(prompt_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdCfg<D>::kSmem);
-  if (e != cudaSuccess) return e;
   prompt_fwd_kernel<D><<<a.plan->n_items, kThreads, FwdCfg<D>::kSmem, s>>>(maps, v);
-  e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.plan->n_joins == 0) return e;
   prompt_join_kernel<D><<<dim3(a.plan->n_joins, a.plan->tiles * 32), 128, 0, s>>>(v);
   return cudaGetLastError();
@@ -433,6 +375,9 @@ cudaError_t launch_d(const PromptArgs& a, const PromptMaps& maps, const PromptDe
 
 cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s) {
   const PromptPlan& p = *a.plan;
+  // first, for it makes the device's context current in this thread, which the tensor maps need
+  const cudaError_t e = p.d == 128 ? set_up<128>() : set_up<64>();
+  if (e != cudaSuccess) return e;
   PromptMaps maps;
   memset(&maps, 0, sizeof(maps));
   PromptDev v{};

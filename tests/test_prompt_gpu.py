@@ -209,6 +209,35 @@ def test_streams_graphs_and_two_calls_of_one_plan(cuda_lib):
     assert sla.read_device_status(plan.device_bytes) == 0
 
 
+def test_from_a_fresh_thread(cuda_lib):
+    """A thread that has made no CUDA call yet has no context current (autograd's threads, a server's)."""
+    import threading
+
+    sla = cuda_lib
+    case = ([90, 20], None, 4, 2, 128, True)
+    q, k, v, do, _, _ = make(case, seed=13)
+    q, k, v, do = q.cuda(), k.cuda(), v.cuda(), do.cuda()
+    plan = plan_of(sla, case)
+    o, lse = sla.prompt_forward(q, k, v, plan)
+    grads = sla.prompt_backward(q, k, v, o, lse, do, plan)
+    out, dx = torch.empty_like(o), tuple(torch.empty_like(t) for t in (q, k, v))
+    got = []
+
+    def work(f):
+        try:
+            got.append(f())
+        except Exception as e:  # noqa: BLE001
+            got.append(e)
+
+    for f in (lambda: sla.prompt_forward(q, k, v, plan, out=out),
+              lambda: sla.prompt_backward(q, k, v, o, lse, do, plan, out=dx)):
+        t = threading.Thread(target=work, args=(f,))
+        t.start()
+        t.join()
+    assert not any(isinstance(x, Exception) for x in got), got
+    assert torch.equal(out, o) and all(torch.equal(a, b) for a, b in zip(dx, grads))
+
+
 def test_refusals(cuda_lib):
     sla = cuda_lib
     case = ([10, 20], None, 4, 2, 64, True)
@@ -227,3 +256,127 @@ def test_refusals(cuda_lib):
     kk = torch.zeros(9000, 2, 64, device="cuda", dtype=torch.bfloat16)
     with pytest.raises(sla.SLAError):
         sla.prompt_forward(q[:1], kk, kk, small, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+def check_grads(case, got, ref, q, k):
+    """dV: P rounded to bf16. dK, dQ: dS rounded to bf16, its D from an O rounded to bf16 (both
+    within the sizes |P dP| + |P| rowsum |dO O|); every exponent off by e; one rounding at the end."""
+    e = score_error(case[4], q, k, 1 / math.sqrt(case[4]))
+    for name, t in zip(("dq", "dk", "dv"), got):
+        rounds = 1 if name == "dv" else 2
+        bound = (rounds * H8 + 4 * e) * ref[name + "_size"] * 1.02 + H8 * ref[name].abs() * 1.02 + 1e-30
+        err = (t.cpu().double() - ref[name]).abs()
+        assert (err <= bound).all(), (name, (err / bound).max())
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_backward(cuda_lib, case):
+    sla = cuda_lib
+    q, k, v, do, lq, lk = make(case, seed=7)
+    plan = plan_of(sla, case, grad=True)
+    ref = R.prompt(q, k, v, lq, lk, case[5], do=do)
+    leaves = [t.cuda().requires_grad_(True) for t in (q, k, v)]
+    o = sla.prompt_attention(*leaves, plan)
+    grads = torch.autograd.grad(o, leaves, do.cuda())
+    assert sla.read_device_status(plan.device_bytes) == 0
+    check_forward(case, o.detach(), None, ref, q, k)
+    check_grads(case, grads, ref, q, k)
+    # bit for bit, again
+    o, lse = sla.prompt_forward(*(t.detach() for t in leaves), plan)
+    again = sla.prompt_backward(*(t.detach() for t in leaves), o, lse, do.cuda(), plan)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+
+def test_backward_with_split_query_tiles(cuda_lib):
+    """Few key tiles that many query tiles see: their sums are split and joined."""
+    sla = cuda_lib
+    for case in (([2500], None, 4, 1, 64, True), ([3000], [140], 2, 1, 128, False)):
+        q, k, v, do, lq, lk = make(case, seed=8)
+        plan = plan_of(sla, case, grad=True)
+        assert plan._backward_workspace > 256 + plan.Tq * plan.Hq * 8  # split sums have a place of their own
+        ref = R.prompt(q, k, v, lq, lk, case[5], do=do)
+        o, lse = sla.prompt_forward(q.cuda(), k.cuda(), v.cuda(), plan)
+        check_grads(case, sla.prompt_backward(q.cuda(), k.cuda(), v.cuda(), o, lse, do.cuda(), plan), ref, q, k)
+
+
+def test_backward_against_differences(cuda_lib):
+    """<grad, w> against the kernel's own central difference."""
+    sla = cuda_lib
+    case = ([140, 9], None, 4, 2, 64, True)
+    q, k, v, do, _, _ = make(case, seed=9)
+    plan = plan_of(sla, case)
+    leaves = [t.cuda().requires_grad_(True) for t in (q, k, v)]
+    grads = torch.autograd.grad(sla.prompt_attention(*leaves, plan), leaves, do.cuda())
+    g = torch.Generator().manual_seed(10)
+    with torch.no_grad():
+        for i, t in enumerate(leaves):
+            # a step in the direction of the gradient: a large difference against the rounding of O
+            w = (grads[i].float() / grads[i].float().norm() * 8).bfloat16()
+            up, down = (t + w), (t - w)
+            w2 = up.double() - down.double()  # the step that bf16 leaves
+            f = [(sla.prompt_attention(*(x if j == i else y for j, y in enumerate(leaves)), plan).double()
+                  * do.cuda().double()).sum() for x in (up, down)]
+            got, want = (f[0] - f[1]).item(), (grads[i].double() * w2).sum().item()
+            # rounding of O: half-steps of both, against dO, adding like noise
+            noise = 2 * H8 * (do.double().norm() * 3).item()
+            assert abs(got - want) <= 0.1 * abs(want) + noise, (i, got, want)
+
+
+def test_backward_keeps_sequences_apart_and_rows_behind_them(cuda_lib):
+    sla = cuda_lib
+    for d in (64, 128):
+        case = ([70, 150, 33], None, 3, 1, d, True)
+        q, k, v, do, lq, _ = make(case, seed=11)
+        plan = plan_of(sla, case)
+        dev = [t.cuda() for t in (q, k, v, do)]
+
+        def grads(ts):
+            o, lse = sla.prompt_forward(*ts[:3], plan)
+            return sla.prompt_backward(*ts[:3], o, lse, ts[3], plan)
+
+        want = grads(dev)
+        keep = torch.ones(253, dtype=torch.bool)
+        keep[70:220] = False
+        bad = [t.clone() for t in dev]
+        for t in bad:
+            t[70:220] = float("nan")
+        for a, b in zip(grads(bad), want):
+            assert torch.equal(a[keep], b[keep])
+        # 19 more tokens of NaN behind the last sequence; gradients land in strided rows
+        long = [torch.cat([t, torch.full((19, *t.shape[1:]), float("nan"), dtype=t.dtype, device="cuda")]) for t in dev]
+        o, lse = sla.prompt_forward(*long[:3], plan)
+        got = sla.prompt_backward(*long[:3], o, lse, long[3], plan)
+        assert all(torch.equal(a[:253], b) and (a[253:] == 0).all() for a, b in zip(got, want))
+        x = torch.full((272, 3 + 1 + 1, d), 9.0, dtype=torch.bfloat16, device="cuda")
+        sla.prompt_backward(*long[:3], o, lse, long[3], plan, out=(x[:, :3], x[:, 3:4], x[:, 4:]))
+        assert torch.equal(x[:253], torch.cat(want, 1)) and (x[253:] == 9.0).all()
+
+
+def test_backward_graph_and_shared_leaves(cuda_lib):
+    sla = cuda_lib
+    case = ([90, 200], None, 4, 2, 128, True)
+    q, k, v, do, _, _ = make(case, seed=12)
+    q, k, v, do = q.cuda(), k.cuda(), v.cuda(), do.cuda()
+    plan = plan_of(sla, case)
+    o, lse = sla.prompt_forward(q, k, v, plan)
+    want = sla.prompt_backward(q, k, v, o, lse, do, plan)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o2, lse2 = sla.prompt_forward(q, k, v, plan)
+        got = sla.prompt_backward(q, k, v, o2, lse2, do, plan)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # k and v the same tensor, and broadcast heads: gradients add up
+    kv = k.clone().requires_grad_(True)
+    (dkv,) = torch.autograd.grad(sla.prompt_attention(q, kv, kv, plan), kv, do)
+    o, lse = sla.prompt_forward(q, k, k, plan)
+    _, dk, dv = sla.prompt_backward(q, k, k, o, lse, do, plan)
+    assert torch.equal(dkv, dk + dv)
+    one = k[:, :1].float().requires_grad_(True)
+    (d1,) = torch.autograd.grad(sla.prompt_attention(q, one.bfloat16().expand(-1, 2, -1), v, plan), one, do)
+    assert d1.shape == one.shape and torch.isfinite(d1).all()
+    # plans for serving refuse the backward
+    serve = sla.prompt_plan([3], [40], Hq=4, Hkv=2, d=128)
+    with pytest.raises(ValueError):
+        sla.prompt_attention(q[:3].clone().requires_grad_(True), k[:40], v[:40], serve)
