@@ -42,7 +42,7 @@ struct PromptDev {
 
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;  // 8 softmax warps, loader, MMA issuer, 2 idle (register split)
 
 template <int D>
 struct FwdCfg {
@@ -53,10 +53,21 @@ struct FwdCfg {
   static constexpr int oKV = 2 * kTileBytes;
   static constexpr int kBytes = oKV + kStages * kTileBytes;
   static constexpr int kSmem = kBytes + 1024;
+  // Of every 8 pairs of exponents, this many are formed on the FMA units: the special
+  // function units take 1024 clocks for a tile's exponentials, its products take 512
+  // (d = 64) or 1024 (d = 128). Measured, 16384 causal tokens, 16 heads, d = 64: none
+  // 675 us, one pair 658, two 635, three 669. At d = 128 (32768 tokens, 12 heads) the
+  // power limit sets the clock and every other count is slower: none 2400 us, two 2430.
+  static constexpr int kFmaPairs = D == 64 ? 2 : 0;
   static constexpr int cO = 256;  // TMEM: S0 S1 (128 columns each), then O0 O1 (D each)
+  // P takes the first 64 columns of its S at d = 128, where TMEM is full: the next S
+  // waits for P V. At d = 64 it has columns of its own, so the next S is formed as soon
+  // as the last one has been read, and the softmax warps never wait for products.
+  static constexpr bool kApart = D == 64;
+  static constexpr int cP = kApart ? 384 : 0, kPStep = kApart ? 64 : 128;
 };
 
-enum { bQ0 = 0, bQ1, bS0, bS1, bP0, bP1, bO0, bO1, bDone, bKV };  // then full / empty of every stage
+enum { bQ0 = 0, bQ1, bS0, bS1, bP0, bP1, bR0, bR1, bX0, bX1, bO0, bO1, bDone, bKV };  // then full / empty of every stage
 
 }  // namespace
 
@@ -103,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     abort_sh = 0;
-    for (int i = 0; i < bKV + 2 * ST; ++i) mbar_init(bar(i), i == bP0 || i == bP1 ? 128 : 1);
+    for (int i = 0; i < bKV + 2 * ST; ++i) mbar_init(bar(i), i >= bP0 && i <= bX1 ? 128 : 1);
     fence_barrier_init();
   }
   if (warp == 9) tmem_alloc(smem_u32(&tmem_base_sh), 512);
@@ -111,12 +122,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tb = tmem_base_sh;
-  // ring position of K (2 s) and V (2 s + 1) of step s
+  // the ring's order: K0, K1, V0, K2, V1, ... - the next step's keys before this step's values
+  auto k_pos = [&](int s) { return s == 0 ? 0 : 2 * s - 1; };
+  auto v_pos = [&](int s) { return min(2 * s + 2, 2 * n - 1); };
   auto full = [&](int i) { return bKV + i % ST; };
   auto empty = [&](int i) { return bKV + ST + i % ST; };
   auto phase = [&](int i) { return uint32_t(i / ST) & 1; };
 
+  // A row's 128 scores stay in its thread's registers: the softmax warps take
+  // what the other four leave (2 x 232 + 40 = 3 x 168, the launch's own share).
   if (warp == 8) {
+    reg_dec<40>();
     if (lane == 0 && n > 0) {
       const int rows = a.G * a.tpt;
       for (int t = 0; t < 2; ++t) {
@@ -130,8 +146,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 2 * n; ++i) {
         if (!wait(empty(i), phase(i) ^ 1)) break;
         issued = i + 1;
-        const int b = bmax - 1 - i / 2;
-        const CUtensorMap* m = (i & 1) ? &maps.v : &maps.k;
+        const bool keys = i == 0 || ((i & 1) && i < 2 * n - 1);
+        const int b = bmax - 1 - (keys ? (i + 1) / 2 : i == 2 * n - 1 ? n - 1 : i / 2 - 1);
+        const CUtensorMap* m = keys ? &maps.k : &maps.v;
         mbar_expect_tx(bar(full(i)), C::kTileBytes);
         for (int s = 0; s < D / 64; ++s)
           tma_load_3d(sb + C::oKV + (i % ST) * C::kTileBytes + s * C::kSub, m, bar(full(i)), s * 64,
@@ -144,12 +161,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 9) {
+    reg_dec<40>();
     constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
     constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
     const int off[2] = {bmax - nb0, bmax - nb1};  // first step of each tile (n: none)
     auto issue_s = [&](int t, int s) {
       if (s == off[t]) wait_w(bQ0 + t, 0);
-      const uint32_t sq = sb + C::oQ + t * C::kTileBytes, sk = sb + C::oKV + ((2 * s) % ST) * C::kTileBytes;
+      const uint32_t sq = sb + C::oQ + t * C::kTileBytes, sk = sb + C::oKV + (k_pos(s) % ST) * C::kTileBytes;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint32_t o = (k >> 2) * C::kSub + (k & 3) * 32;
@@ -157,55 +175,88 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mma_commit(bar(bS0 + t));
     };
-    if (n > 0) {
-      wait_w(full(0), phase(0));
+    auto have_k = [&](int s) {
+      wait_w(full(k_pos(s)), phase(k_pos(s)));
       tc_fence_after();
+    };
+    if (n > 0) {
+      have_k(0);
       for (int t = 0; t < 2; ++t)
         if (off[t] == 0) issue_s(t, 0);
       mma_commit(bar(empty(0)));
     }
     for (int s = 0; s < n; ++s) {
-      const int iv = 2 * s + 1;
+      const int iv = v_pos(s);
       const uint32_t sv = sb + C::oKV + (iv % ST) * C::kTileBytes;
-      wait_w(full(iv), phase(iv));
-      const int valid = it.lk - (bmax - 1 - s) * 128;
-      if (valid < 128) {
-        // the sequence ends inside this block: the rows behind it are another sequence's (0 x NaN is NaN)
-        for (int x = valid * 8 + lane; x < 128 * 8; x += 32)
+      auto have_v = [&]() {
+        wait_w(full(iv), phase(iv));
+        const int valid = it.lk - (bmax - 1 - s) * 128;
+        if (valid < 128) {
+          // the sequence ends inside this block: the rows behind it are another sequence's (0 x NaN is NaN)
+          for (int x = valid * 8 + lane; x < 128 * 8; x += 32)
 #pragma unroll
-          for (int sub = 0; sub < D / 64; ++sub)
-            *reinterpret_cast<uint4*>(smem + C::oKV + (iv % ST) * C::kTileBytes + sub * C::kSub + x * 16) =
-                make_uint4(0, 0, 0, 0);
-        fence_async_smem();
-        __syncwarp();
-      }
-      bool have_k = false;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (s >= off[t]) {
-          const int i = s - off[t];
+            for (int sub = 0; sub < D / 64; ++sub)
+              *reinterpret_cast<uint4*>(smem + C::oKV + (iv % ST) * C::kTileBytes + sub * C::kSub + x * 16) =
+                  make_uint4(0, 0, 0, 0);
+          fence_async_smem();
+          __syncwarp();
+        }
+      };
+      auto issue_o = [&](int t) {
+        const int i = s - off[t];
+        if (!C::kApart) {
           wait_w(bP0 + t, i & 1);
           tc_fence_after();
+        }
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_bf16_ts(tb + C::cO + t * D, tb + t * 128 + k * 8, sdesc(sv + k * 2048, C::kSub, 1024), idO,
-                        (i > 0 || k > 0) ? 1u : 0u);
-          mma_commit(bar(bO0 + t));
+        for (int k = 0; k < 8; ++k) {
+          if (k == (C::kApart ? 0 : 4)) {
+            wait_w(bR0 + t, i & 1);
+            tc_fence_after();
+          }
+          mma_bf16_ts(tb + C::cO + t * D, tb + C::cP + t * C::kPStep + k * 8, sdesc(sv + k * 2048, C::kSub, 1024), idO,
+                      (i > 0 || k > 0) ? 1u : 0u);
         }
-        if (s + 1 < n && s + 1 >= off[t]) {
-          if (!have_k) wait_w(full(2 * s + 2), phase(2 * s + 2));
-          have_k = true;
-          tc_fence_after();
-          issue_s(t, s + 1);
+        mma_commit(bar(bO0 + t));
+      };
+      if (C::kApart) {
+        if (s + 1 < n) {
+          have_k(s + 1);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (s >= off[t]) {  // S of this step has been read
+              wait_w(bX0 + t, (s - off[t]) & 1);
+              tc_fence_after();
+            }
+            if (s + 1 >= off[t]) issue_s(t, s + 1);
+          }
+          mma_commit(bar(empty(k_pos(s + 1))));
         }
+        have_v();
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (s >= off[t]) issue_o(t);
+      } else {
+        have_v();
+        bool have = false;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (s >= off[t]) issue_o(t);
+          if (s + 1 < n && s + 1 >= off[t]) {
+            if (!have) have_k(s + 1);
+            have = true;
+            issue_s(t, s + 1);
+          }
+        }
+        if (s + 1 < n) mma_commit(bar(empty(k_pos(s + 1))));
       }
       mma_commit(bar(empty(iv)));
-      if (s + 1 < n) mma_commit(bar(empty(2 * s + 2)));
     }
     mma_commit(bar(bDone));
     wait_drain(bDone, 0);
     __syncwarp();
-  } else {
+  } else if (warp < 8) {
+    reg_inc<232>();
     const int t = warp >> 2, r = threadIdx.x & 127;
     const int nb = t == 0 ? nb0 : nb1, steps = nb - it.b0;
     const int tok = t * a.tpt + r / a.G, g = r - (r / a.G) * a.G;
@@ -214,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int limit = !live ? 0 : a.causal ? int(max(0LL, min((long long)it.lk, (long long)it.pos0 + tok + 1))) : it.lk;
     const int warp_limit = __reduce_min_sync(0xffffffffu, limit);
     const uint32_t tq = tb + (uint32_t(32 * (warp & 3)) << 16);
-    const uint32_t tS = tq + t * 128, tO = tq + C::cO + t * D;
+    const uint32_t tS = tq + t * 128, tP = tq + C::cP + t * C::kPStep, tO = tq + C::cO + t * D;
     const float c = a.scale_log2;
     const float slack = 8.0f / c;
     float m = -INFINITY, l = 0.0f;
@@ -226,6 +277,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < 4; ++j) tmem_ld32(tS + 32 * j, *reinterpret_cast<float(*)[32]>(&s[32 * j]));
       tmem_wait_ld();
+      if (C::kApart) {
+        tc_fence_before();
+        mbar_arrive(bar(bX0 + t));
+      }
       if (key0 + 128 > warp_limit) {
         const int seen = limit - key0;
 #pragma unroll
@@ -233,8 +288,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int j = 4; j < 128; ++j) mx[j & 3] = max_nan(mx[j & 3], s[j]);
-      const float top = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3]));
+      for (int j = 4; j < 124; j += 8)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) mx[x] = max3_nan(mx[x], s[j + 2 * x], s[j + 2 * x + 1]);
+      mx[0] = max3_nan(mx[0], s[124], s[125]);
+      mx[1] = max3_nan(mx[1], s[126], s[127]);
+      const float top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]);
       const bool raise = !(top <= m + slack);  // NaN raises: the row becomes NaN
       if (__any_sync(0xffffffffu, raise)) {
         const float f = raise && m != -INFINITY ? ex2((m - top) * c) : 1.0f;
@@ -255,21 +314,50 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_st();
         }
       }
-      const float mc = m == -INFINITY ? 0.0f : -m * c;
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      uint32_t p[64];
-#pragma unroll
-      for (int j = 0; j < 128; j += 2) {
-        const float x = ex2(fmaf(s[j], c, mc)), y = ex2(fmaf(s[j + 1], c, mc));
-        sum[(j >> 1) & 3] += x + y;
-        p[j >> 1] = pack_bf16(x, y);
+      if (C::kApart && i > 0) {  // P of the block before has been read
+        wait_w(bO0 + t, (i - 1) & 1);
+        tc_fence_after();
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_st32u(tS, p);
-      tmem_st32u(tS + 32, p + 32);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(bar(bP0 + t));
+      const float mc = m == -INFINITY ? 0.0f : -m * c;
+      const uint64_t c2 = two(c, c), mc2 = two(mc, mc);
+      uint64_t sum[4] = {two(l, 0.0f), 0, 0, 0};
+      auto form = [&](int from, int to) {  // P = 2^(c s - c m), in place
+#pragma unroll
+        for (int j = from; j < to; j += 2) {
+          const uint64_t x = fma2(two(s[j], s[j + 1]), c2, mc2);
+          if ((j >> 1) % 8 >= 8 - C::kFmaPairs) {
+            ex2_fma(x, s[j], s[j + 1]);
+          } else {
+            untwo(x, s[j], s[j + 1]);
+            s[j] = ex2(s[j]);
+            s[j + 1] = ex2(s[j + 1]);
+          }
+          if (C::kApart) sum[(j >> 1) & 3] = add2(sum[(j >> 1) & 3], two(s[j], s[j + 1]));
+        }
+#pragma unroll
+        for (int j = from; j < to; j += 32) {
+          uint32_t p[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) p[x] = pack_bf16(s[j + 2 * x], s[j + 2 * x + 1]);
+          tmem_st16u(tP + j / 2, p);
+        }
+      };
+      auto hand_over = [&](int b) {
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(b + t));
+      };
+      form(0, 64);
+      if (!C::kApart) hand_over(bP0);  // half of P V runs while the other half of P is formed
+      form(64, 128);
+      hand_over(bR0);
+      if (!C::kApart) {  // off the chain to the next product
+#pragma unroll
+        for (int j = 0; j < 128; j += 2) sum[(j >> 1) & 3] = add2(sum[(j >> 1) & 3], two(s[j], s[j + 1]));
+      }
+      float x, y;
+      untwo(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
+      l = x + y;
     }
     if (steps > 0) {
       wait_w(bO0 + t, (steps - 1) & 1);
@@ -310,6 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       else if (a.lse)
         a.lse[token * a.Hq + head] = lse2 * 0.6931471805599453f;
     }
+  } else {
+    reg_dec<40>();
   }
   tc_fence_before();
   __syncthreads();

@@ -52,6 +52,51 @@ template <int n>
 __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n));
 }
+// max that keeps NaN
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// two float32 values in one register pair, and the packed operations on them
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void untwo(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 2^x of two values on the FMA units, for x <= 127: x = i + f with i the nearest
+// whole number (adding 1.5 2^23 rounds to it), 2^f by a cubic with p(0) = 1 fitted
+// to the least relative error on [-1/2, 1/2] (1.0e-4, a twentieth of a bf16 step),
+// i added to the exponent: x <= -127 gives 0 (the exponent of 1 less 127). Not for NaN.
+__device__ __forceinline__ void ex2_fma(uint64_t x2, float& lo, float& hi) {
+  float x, y;
+  untwo(x2, x, y);
+  const uint64_t v = two(fmaxf(x, -127.0f), fmaxf(y, -127.0f));
+  constexpr float kRound = 12582912.0f;
+  const uint64_t t = add2(v, two(kRound, kRound));
+  const uint64_t f = fma2(add2(t, two(-kRound, -kRound)), two(-1.0f, -1.0f), v);
+  uint64_t p = fma2(f, two(0.05500893294811249f, 0.05500893294811249f), two(0.2422109693288803f, 0.2422109693288803f));
+  p = fma2(p, f, two(0.6932829022407532f, 0.6932829022407532f));
+  p = fma2(p, f, two(1.0f, 1.0f));
+  float a, b, i, j;
+  untwo(p, a, b);
+  untwo(t, i, j);
+  lo = __int_as_float(__float_as_int(a) + (__float_as_int(i) << 23));
+  hi = __int_as_float(__float_as_int(b) + (__float_as_int(j) << 23));
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
