@@ -42,24 +42,28 @@ constexpr int kSub = 128 * 128;  // 128 rows x 128 bytes (64 columns)
 
 }  // namespace
 
-// (lse log2 e, D) of every query row, [key head][token G + g]. One warp per row. Bound: reading O and dO.
+// (lse log2 e, D) of every query row, [key head][token G + g]. d / 8 lanes per row,
+// 16 bytes each. Bound: reading O and dO.
 template <int D>
 __global__ void __launch_bounds__(256) prompt_rowsum_kernel(const PromptGradDev a) {
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= a.Tq * a.Hq) return;
-  const int lane = threadIdx.x & 31;
-  const long long t = row / a.Hq;
-  const int h = int(row - t * a.Hq);
-  const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(a.o.base) + t * a.o.row + h * a.o.head + lane * (D / 32);
-  const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.g.base) + t * a.g.row + h * a.g.head + lane * (D / 32);
+  constexpr int kLanes = D / 8;
+  const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / kLanes;
+  const int lane = threadIdx.x % kLanes;
+  const bool live = row < a.Tq * a.Hq;
+  const long long t = live ? row / a.Hq : 0;
+  const int h = live ? int(row - t * a.Hq) : 0;
   float sum = 0.0f;
+  if (live) {
+    const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.o.base) + t * a.o.row +
+                                                    h * a.o.head + lane * 8);
+    const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.g.base) + t * a.g.row +
+                                                    h * a.g.head + lane * 8);
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-  for (int i = 0; i < D / 32; i += 2) {
-    const uint32_t x = *reinterpret_cast<const uint32_t*>(o + i), y = *reinterpret_cast<const uint32_t*>(g + i);
-    sum += bf16_lo(x) * bf16_lo(y) + bf16_hi(x) * bf16_hi(y);
+    for (int i = 0; i < 4; ++i) sum += bf16_lo(u[i]) * bf16_lo(v[i]) + bf16_hi(u[i]) * bf16_hi(v[i]);
   }
-  for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-  if (lane == 0) {
+  for (int s = kLanes / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+  if (live && lane == 0) {
     const int hk = h / a.G;
     a.ld[hk * (a.Tq * a.G) + t * a.G + (h - hk * a.G)] = make_float2(a.lse[t * a.Hq + h] * kLog2e, sum);
   }
@@ -70,6 +74,11 @@ __global__ void __launch_bounds__(256) prompt_rowsum_kernel(const PromptGradDev 
 // that see it. Per query tile i:
 //   S^T = K Q_i^T, dP^T = V dO_i^T      (M = 128 keys, N = 128 query rows, K = d)
 //   dV += P^T dO_i, dK += dS^T Q_i      (M = 128 keys, N = d, K = 128; A in TMEM)
+// A query row's lse and D belong to a column here, which every thread would have to
+// fetch from shared memory (64 vector loads per thread and tile, a quarter of the
+// bandwidth that the products' operands need). They go into the products instead: one
+// more K step of 16 whose A is (1, 1, 1, 0 ...) and whose B holds -lse / scale, or -D,
+// as three bf16 that add up to its float32, gives S - lse / scale and dP - D.
 // Warps 0-3 form columns 0-63 of P^T and dS^T, warps 4-7 columns 64-127; warp 8
 // loads, warp 9 issues. While the tensor cores run dV_i and S^T_{i+1} the warps
 // form dS_i, while they run dK_i and dP^T_{i+1} the warps form P_{i+1}.
@@ -82,9 +91,13 @@ struct KeyCfg {
   static constexpr int kStages = 2;
   static constexpr int oK = 0, oV = kTileBytes, oQ = 2 * kTileBytes;
   static constexpr int oG = oQ + kStages * kTileBytes;
-  static constexpr int oL = oG + kStages * kTileBytes;  // (lse2, D) of the stage's 128 rows
-  static constexpr int kBytes = oL + kStages * 1024;
+  // the extra K steps: [2 column octets][128 rows][8] bf16, not swizzled
+  static constexpr int kStep = 4096;
+  static constexpr int oOne = oG + kStages * kTileBytes;  // A, constant
+  static constexpr int oL = oOne + kStep;                 // B of S and of dP, per stage
+  static constexpr int kBytes = oL + kStages * 2 * kStep;
   static constexpr int kSmem = kBytes + 1024;
+  static constexpr int kFmaPairs = 2;  // of every 8 pairs of exponentials, formed on the FMA units
   static constexpr int cS = 0, cP = 128, cV = 256, cK = 256 + D;  // TMEM columns
 };
 enum { kbKV = 0, kbS, kbP, kbPr, kbDr, kbDone, kbL0, kbL1, kbQ };  // then Q, dO full / empty of every stage
@@ -136,6 +149,11 @@ __global__ void __launch_bounds__(320, 1)
     for (int i = 0; i < kbQ + 4 * ST; ++i) mbar_init(bar(i), i == kbPr || i == kbDr ? 256 : i == kbL0 || i == kbL1 ? 32 : 1);
     fence_barrier_init();
   }
+  for (int x = threadIdx.x; x < (1 + 2 * ST) * (C::kStep / 16); x += 320) {
+    const bool one = x < 128;  // 1.0 in bf16 is 0x3f80
+    *reinterpret_cast<uint4*>(smem + C::oOne + x * 16) = make_uint4(one ? 0x3f803f80u : 0u, one ? 0x3f80u : 0u, 0, 0);
+  }
+  fence_async_smem();
   // rows that the query tiles' copies never write (128 is not a multiple of G): their products must add nothing
   if (rows < 128) {
     const int idle = (128 - rows) * 8;
@@ -161,6 +179,20 @@ __global__ void __launch_bounds__(320, 1)
         }
       }
       const float2* ld = a.ld + it.head * (a.Tq * a.G);
+      const float inv_c = 1.0f / a.scale_log2;
+      // (lse2, D) of a tile, fetched a tile ahead: four rows per lane
+      float2 next[4];
+      auto fetch = [&](int i) {
+        const int tok = (it.t0 + i) * a.tpt;
+        const long long r0 = (it.q0 + (long long)tok) * a.G;
+        const int have = i < n ? min(rows, (it.lq - tok) * a.G) : 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = j * 32 + lane;
+          next[j] = r < have ? ld[r0 + r] : make_float2(0.0f, 0.0f);
+        }
+      };
+      fetch(0);
       int qi = 0, gi = 0;
       for (int i = 0; i < n; ++i) {
         const int tok = (it.t0 + i) * a.tpt;
@@ -172,6 +204,19 @@ __global__ void __launch_bounds__(320, 1)
             tma_load_4d(sb + C::oQ + (i % ST) * C::kTileBytes + s * kSub, &maps.q, bar(qfull(i)), s * 64, 0,
                         it.q0 + tok, it.head);
         }
+        __syncwarp();
+        // the stage's -lse / scale and -D: its last readers, S and dP, came before the dK that freed the stage
+        unsigned char* to = smem + C::oL + (i % ST) * 2 * C::kStep;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = j * 32 + lane;
+          // (a row that sees no key has lse = -inf; all its columns are masked)
+          *reinterpret_cast<uint4*>(to + r * 16) = three_bf16(next[j].x == -INFINITY ? 0.0f : -next[j].x * inv_c);
+          *reinterpret_cast<uint4*>(to + C::kStep + r * 16) = three_bf16(-next[j].y);
+        }
+        fence_async_smem();
+        mbar_arrive(bar(i % ST == 0 ? kbL0 : kbL1));
+        fetch(i + 1);
         if (!wait_w(gempty(i), phase(i) ^ 1)) break;
         if (lane == 0) {
           gi = i + 1;
@@ -180,16 +225,6 @@ __global__ void __launch_bounds__(320, 1)
             tma_load_4d(sb + C::oG + (i % ST) * C::kTileBytes + s * kSub, &maps.g, bar(gfull(i)), s * 64, 0,
                         it.q0 + tok, it.head);
         }
-        // the stage's (lse2, D): freed with its Q (its last reader, dK, comes after dS)
-        float2* to = reinterpret_cast<float2*>(smem + C::oL + (i % ST) * 1024);
-        const long long r0 = (it.q0 + (long long)tok) * a.G;
-        const int have = min(rows, (it.lq - tok) * a.G);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = j * 32 + lane;
-          to[r] = r < have ? ld[r0 + r] : make_float2(0.0f, 0.0f);
-        }
-        mbar_arrive(bar(i % ST == 0 ? kbL0 : kbL1));
       }
       if (lane == 0) {
         wait_drain(kbKV, 0);
@@ -212,25 +247,28 @@ __global__ void __launch_bounds__(320, 1)
       fence_async_smem();
       __syncwarp();
     };
-    auto issue_wide = [&](int col, int a_off, int b_off) {  // [128 keys][d] x [128 rows][d]^T
+    auto issue_wide = [&](int col, int a_off, int b_off, int ext) {  // [128 keys][d] x [128 rows][d]^T
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint32_t o = (k >> 2) * kSub + (k & 3) * 32;
         mma_bf16(tb + col, sdesc(sb + a_off + o, 16, 1024), sdesc(sb + b_off + o, 16, 1024), idS, k > 0);
       }
+      // no swizzle: 8 x 16-byte core matrices, 2048 bytes apart along K, 128 along the rows
+      mma_bf16(tb + col, sdesc(sb + C::oOne, 2048, 128, 0), sdesc(sb + ext, 2048, 128, 0), idS, 1);
     };
     auto issue_s = [&](int i) {
+      wait_w(i % ST == 0 ? kbL0 : kbL1, phase(i));
       wait_w(qfull(i), phase(i));
       clear_tail(i, C::oQ);
       tc_fence_after();
-      issue_wide(C::cS, C::oK, C::oQ + (i % ST) * C::kTileBytes);
+      issue_wide(C::cS, C::oK, C::oQ + (i % ST) * C::kTileBytes, C::oL + (i % ST) * 2 * C::kStep);
       mma_commit(bar(kbS));
     };
     auto issue_p = [&](int i) {
       wait_w(gfull(i), phase(i));
       clear_tail(i, C::oG);
       tc_fence_after();
-      issue_wide(C::cP, C::oV, C::oG + (i % ST) * C::kTileBytes);
+      issue_wide(C::cP, C::oV, C::oG + (i % ST) * C::kTileBytes, C::oL + ((i % ST) * 2 + 1) * C::kStep);
       mma_commit(bar(kbP));
     };
     // A: packed columns 0-31 (rows 0-63 of the tile) and 64-95 (rows 64-127) of the region it overwrote
@@ -266,7 +304,7 @@ __global__ void __launch_bounds__(320, 1)
     const bool live = key < it.lk;
     const uint32_t tq = tb + (uint32_t(32 * (warp & 3)) << 16);
     const uint32_t tS = tq + C::cS + half * 64, tP = tq + C::cP + half * 64;
-    const float c = a.scale_log2;
+    const uint64_t c2 = two(a.scale_log2, a.scale_log2);
     for (int i = 0; i < n; ++i) {
       const int tok = (it.t0 + i) * a.tpt;
       // columns (packed query rows) lo .. hi - 1 of this half see the key
@@ -274,8 +312,6 @@ __global__ void __launch_bounds__(320, 1)
       const int lo = int(max(0LL, min(128LL, first * a.G))) - half * 64;
       const int hi = min(rows, (it.lq - tok) * a.G) - half * 64;
       const bool masked = lo > 0 || hi < 64;
-      const float4* ld = reinterpret_cast<const float4*>(smem + C::oL + (i % ST) * 1024 + half * 512);
-      wait_w(i % ST == 0 ? kbL0 : kbL1, phase(i));
       wait_w(kbS, i & 1);
       tc_fence_after();
       float p[64];
@@ -283,10 +319,15 @@ __global__ void __launch_bounds__(320, 1)
       tmem_ld32(tS + 32, *reinterpret_cast<float(*)[32]>(&p[32]));
       tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 64; j += 2) {
-        const float4 w = ld[j >> 1];
-        p[j] = ex2(fmaf(p[j], c, -w.x));
-        p[j + 1] = ex2(fmaf(p[j + 1], c, -w.z));
+      for (int j = 0; j < 64; j += 2) {  // 2^(c S - lse2)
+        const uint64_t x = mul2(two(p[j], p[j + 1]), c2);
+        if ((j >> 1) % 8 >= 8 - C::kFmaPairs) {
+          ex2_fma(x, p[j], p[j + 1]);
+        } else {
+          untwo(x, p[j], p[j + 1]);
+          p[j] = ex2(p[j]);
+          p[j + 1] = ex2(p[j + 1]);
+        }
       }
       if (__any_sync(0xffffffffu, masked)) {
 #pragma unroll
@@ -307,11 +348,8 @@ __global__ void __launch_bounds__(320, 1)
         tmem_ld32(tP + 32 * q, x);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const float4 v = ld[16 * q + (j >> 1)];
-          p[32 * q + j] *= x[j] - v.y;
-          p[32 * q + j + 1] *= x[j + 1] - v.w;
-        }
+        for (int j = 0; j < 32; j += 2)
+          untwo(mul2(two(p[32 * q + j], p[32 * q + j + 1]), two(x[j], x[j + 1])), p[32 * q + j], p[32 * q + j + 1]);
       }
       if (__any_sync(0xffffffffu, masked)) {
 #pragma unroll
@@ -672,7 +710,7 @@ template <int D>
 cudaError_t launch_d(const PromptGradArgs& a, const PromptGradMaps& maps, const PromptGradDev& v, cudaStream_t s) {
   const PromptPlan& p = *a.plan;
   const long long rows = p.Tq * p.Hq;
-  prompt_rowsum_kernel<D><<<unsigned((rows + 7) / 8), 256, 0, s>>>(v);
+  prompt_rowsum_kernel<D><<<unsigned((rows * (D / 8) + 255) / 256), 256, 0, s>>>(v);
   if (p.n_keys > 0) prompt_bwd_keys_kernel<D><<<p.n_keys, 320, KeyCfg<D>::kSmem, s>>>(maps, v);
   if (p.n_kjoins > 0) prompt_keys_join_kernel<D><<<dim3(p.n_kjoins, 32, 2), 128, 0, s>>>(v);
   prompt_bwd_rows_kernel<D><<<p.n_rows, 384, RowCfg<D>::kSmem, s>>>(maps, v);

@@ -53,6 +53,11 @@ __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n));
 }
 // max that keeps NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float y;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
@@ -72,19 +77,32 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// x as three bf16 that add up to it, and zeros, as one 16-byte row piece (inf and NaN as they are)
+__device__ __forceinline__ uint4 three_bf16(float x) {
+  const float a = bf16_lo(pack_bf16(x, 0.0f));
+  const float y = fabsf(a) < INFINITY ? x - a : 0.0f;
+  const float b = bf16_lo(pack_bf16(y, 0.0f));
+  return make_uint4(pack_bf16(a, b), pack_bf16(y - b, 0.0f), 0, 0);
+}
 // 2^x of two values on the FMA units, for x <= 127: x = i + f with i the nearest
 // whole number (adding 1.5 2^23 rounds to it), 2^f by a cubic with p(0) = 1 fitted
 // to the least relative error on [-1/2, 1/2] (1.0e-4, a twentieth of a bf16 step),
-// i added to the exponent: x <= -127 gives 0 (the exponent of 1 less 127). Not for NaN.
+// i added to the exponent: x <= -127 gives 0 (the exponent of 1 less
+// 127); NaN gives a number near the largest.
 __device__ __forceinline__ void ex2_fma(uint64_t x2, float& lo, float& hi) {
   float x, y;
   untwo(x2, x, y);
-  const uint64_t v = two(fmaxf(x, -127.0f), fmaxf(y, -127.0f));
+  const uint64_t v = two(max_nan(x, -127.0f), max_nan(y, -127.0f));
   constexpr float kRound = 12582912.0f;
   const uint64_t t = add2(v, two(kRound, kRound));
   const uint64_t f = fma2(add2(t, two(-kRound, -kRound)), two(-1.0f, -1.0f), v);
@@ -96,11 +114,6 @@ __device__ __forceinline__ void ex2_fma(uint64_t x2, float& lo, float& hi) {
   untwo(t, i, j);
   lo = __int_as_float(__float_as_int(a) + (__float_as_int(i) << 23));
   hi = __int_as_float(__float_as_int(b) + (__float_as_int(j) << 23));
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
 }
 
 // ---- host: tensor maps of packed tokens ----
