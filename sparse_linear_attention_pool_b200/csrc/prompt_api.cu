@@ -76,11 +76,12 @@ std::vector<PromptItem> row_items(const sla_prompt_params& p, int per) {
   return out;
 }
 
-// Time at which the last SM ends, blocks of cost (key blocks + overhead) dispatched longest first.
-double makespan(std::vector<double> cost) {
+// Time at which the last of `places` ends, items dispatched longest first.
+double makespan(std::vector<double> cost, int places) {
   std::sort(cost.begin(), cost.end(), std::greater<double>());
+  if (int(cost.size()) <= places) return cost.empty() ? 0.0 : cost[0];
   std::priority_queue<double, std::vector<double>, std::greater<double>> sm;
-  for (int i = 0; i < kPromptSms; ++i) sm.push(0.0);
+  for (int i = 0; i < places; ++i) sm.push(0.0);
   double last = 0.0;
   for (double c : cost) {
     const double e = sm.top() + c;
@@ -94,20 +95,43 @@ double makespan(std::vector<double> cost) {
 // Pieces that an item of n blocks is cut into for pieces of about `chunk` blocks.
 int pieces(int n, int chunk) { return chunk <= 0 || n <= chunk ? 1 : (n + chunk - 1) / chunk; }
 
-// Costs in units of one key block of a two-tile item.
-constexpr double kItemCost = 3.0;      // start, first loads and the store
-constexpr double kOneTile = 0.8;       // a step of a one-tile item
-constexpr double kJoinCost = 4.0;      // the second launch
+// The smallest chunk (of at least 4 blocks) that cuts items of these lengths into at most
+// `most` pieces: pieces that fill whole rounds over the SMs' places and start no further one.
+int chunk_for(const std::vector<int>& lengths, int most) {
+  int lo = 4, hi = 4;
+  for (int n : lengths) hi = std::max(hi, n);
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    long long parts = 0;
+    for (int n : lengths) parts += pieces(n, mid);
+    if (parts <= most)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
 
-double split_cost(const std::vector<PromptItem>& items, int chunk, double step) {
+// Costs in units of one key block of a two-tile item, the only one on its SM.
+constexpr double kItemCost = 3.0;  // start, first loads and the store
+constexpr double kOneTile = 1.0;   // a step of a one-tile item, two of which share an SM
+constexpr double kAlone = 0.7;     // and of one that has its SM to itself
+constexpr double kJoinCost = 3.0;  // the second launch
+
+// full_rows: how full of live rows the tiles are
+double split_cost(const std::vector<PromptItem>& items, int chunk, int tiles, double full_rows) {
   std::vector<double> cost;
-  bool any = false;
+  size_t parts = 0;
+  for (const PromptItem& it : items) parts += pieces(it.b1, chunk);
+  const bool shared = tiles == 1 && parts > size_t(kPromptSms);
+  const double step = tiles == 2 ? 1.0 : shared ? kOneTile : kAlone;
+  double joins = 0.0;  // rows of partial results, in tiles: written and read once more in float32
   for (const PromptItem& it : items) {
     const int n = pieces(it.b1, chunk);
-    any = any || n > 1;
+    if (n > 1) joins += n * tiles;
     for (int i = 0; i < n; ++i) cost.push_back(kItemCost + step * ((it.b1 + n - 1) / n));
   }
-  return makespan(cost) + (any ? kJoinCost : 0.0);
+  return makespan(cost, shared ? 2 * kPromptSms : kPromptSms) + (joins > 0.0 ? kJoinCost + full_rows * joins / kPromptSms : 0.0);
 }
 
 void add_backward(const sla_prompt_params& p, Lists& L);
@@ -124,15 +148,14 @@ Lists make_lists(const sla_prompt_params& p) {
   std::vector<PromptItem> base;
   for (int tiles = longest <= tpt ? 1 : 2; tiles >= 1; --tiles) {
     std::vector<PromptItem> items = row_items(p, tiles * tpt);
-    const double step = tiles == 2 ? 1.0 : kOneTile;
     std::vector<int> chunks = {0};
     if (items.size() < 4 * kPromptSms) {
-      long long total = 0;
-      for (const PromptItem& it : items) total += it.b1;
-      for (int w : {1, 2, 3, 4, 6}) chunks.push_back(int(std::max(4LL, total / (kPromptSms * w) + 1)));
+      std::vector<int> lengths;
+      for (const PromptItem& it : items) lengths.push_back(it.b1);
+      for (int rounds = 1; rounds <= 3; ++rounds) chunks.push_back(chunk_for(lengths, rounds * kPromptSms * (3 - tiles)));
     }
     for (int chunk : chunks) {
-      const double c = split_cost(items, chunk, step);
+      const double c = split_cost(items, chunk, tiles, std::min(1.0, double(longest) / tpt));
       if (base.empty() || c < best) {
         best = c;
         best_chunk = chunk;
@@ -172,7 +195,7 @@ void add_backward(const sla_prompt_params& p, Lists& L) {
   for (int tiles = 2; tiles >= 1; --tiles) {
     std::vector<PromptItem> rows = row_items(p, tiles * tpt);
     if (tiles == 1 && rows.size() >= 8 * kPromptSms) break;
-    const double c = split_cost(rows, 0, tiles == 2 ? 1.0 : kOneTile);
+    const double c = split_cost(rows, 0, 2, 1.0) * (tiles == 2 ? 1.0 : 0.8);  // one CTA per SM either way
     if (tiles == 2 || c < best) {
       best = c;
       L.rows = std::move(rows);
@@ -183,7 +206,6 @@ void add_backward(const sla_prompt_params& p, Lists& L) {
 
   std::vector<PromptKeys> base;
   int q0 = 0, k0 = 0;
-  long long total = 0;
   for (int s = 0; s < p.n_seq; ++s) {
     const int lq = p.len_q[s], lk = p.len_k ? p.len_k[s] : lq;
     const int tiles = (lq + tpt - 1) / tpt;
@@ -201,15 +223,17 @@ void add_backward(const sla_prompt_params& p, Lists& L) {
         it.t0 = int(std::min<long long>(tiles, first / tpt));
         it.t1 = tiles;
         it.slot = -1;
-        total += it.t1 - it.t0;
         base.push_back(it);
       }
     q0 += lq;
     k0 += lk;
   }
   std::vector<int> chunks = {0};
-  if (base.size() < 4 * kPromptSms)
-    for (int w : {1, 2, 3}) chunks.push_back(int(std::max(4LL, total / (kPromptSms * w) + 1)));
+  if (base.size() < 4 * kPromptSms) {
+    std::vector<int> lengths;
+    for (const PromptKeys& it : base) lengths.push_back(it.t1 - it.t0);
+    for (int rounds = 1; rounds <= 3; ++rounds) chunks.push_back(chunk_for(lengths, rounds * kPromptSms));
+  }
   int chunk = 0;
   best = -1.0;
   for (int c : chunks) {
@@ -220,7 +244,7 @@ void add_backward(const sla_prompt_params& p, Lists& L) {
       any = any || n > 1;
       for (int i = 0; i < n; ++i) cost.push_back(kItemCost + double((it.t1 - it.t0 + n - 1) / n));
     }
-    const double m = makespan(cost) + (any ? kJoinCost : 0.0);
+    const double m = makespan(cost, kPromptSms) + (any ? kJoinCost : 0.0);
     if (best < 0.0 || m < best) {
       best = m;
       chunk = c;
@@ -264,6 +288,10 @@ size_t layout(const sla_prompt_params& p, const Lists& L, PromptPlan* h) {
   h->n_items = int(L.items.size());
   h->n_joins = int(L.joins.size());
   h->n_slots = L.slots;
+  for (const PromptJoin& j : L.joins) {
+    const int tpt = kPromptTile / h->G;
+    h->join_rows = std::max(h->join_rows, j.nq > tpt ? kPromptTile + (j.nq - tpt) * h->G : j.nq * h->G);
+  }
   h->n_keys = int(L.keys.size());
   h->n_kjoins = int(L.kjoins.size());
   h->n_kslots = L.kslots;

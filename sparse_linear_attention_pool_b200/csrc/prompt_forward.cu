@@ -42,15 +42,18 @@ struct PromptDev {
 
 namespace {
 
-constexpr int kThreads = 384;  // 8 softmax warps, loader, MMA issuer, 2 idle (register split)
 
-template <int D>
+template <int D, int TILES>
 struct FwdCfg {
   static constexpr int kSub = 128 * 128;             // 128 rows x 128 bytes (64 columns)
   static constexpr int kTileBytes = kSub * (D / 64);  // 128 x D bf16
-  static constexpr int kStages = D == 128 ? 4 : 8;   // K and V tiles in the ring
+  // Two tiles: one CTA per SM (8 softmax warps, loader, MMA issuer, two idle ones that
+  // give up registers). One tile: two CTAs per SM, each with half the ring and TMEM.
+  static constexpr int kSoft = 4 * TILES, kThreads = TILES == 2 ? 384 : 192;
+  static constexpr int kCtas = TILES == 2 ? 1 : 2;
+  static constexpr int kStages = D == 128 ? (TILES == 2 ? 4 : 2) : (TILES == 2 ? 8 : 5);  // K and V tiles in the ring
   static constexpr int oQ = 0;
-  static constexpr int oKV = 2 * kTileBytes;
+  static constexpr int oKV = TILES * kTileBytes;
   static constexpr int kBytes = oKV + kStages * kTileBytes;
   static constexpr int kSmem = kBytes + 1024;
   // Of every 8 pairs of exponents, this many are formed on the FMA units: the special
@@ -59,22 +62,24 @@ struct FwdCfg {
   // 675 us, one pair 658, two 635, three 669. At d = 128 (32768 tokens, 12 heads) the
   // power limit sets the clock and every other count is slower: none 2400 us, two 2430.
   static constexpr int kFmaPairs = D == 64 ? 2 : 0;
-  static constexpr int cO = 256;  // TMEM: S0 S1 (128 columns each), then O0 O1 (D each)
+  // TMEM columns: S of every tile (128 each), O of every tile (D each).
   // P takes the first 64 columns of its S at d = 128, where TMEM is full: the next S
   // waits for P V. At d = 64 it has columns of its own, so the next S is formed as soon
   // as the last one has been read, and the softmax warps never wait for products.
+  static constexpr int kCols = 256 * TILES;
+  static constexpr int cO = 128 * TILES;
   static constexpr bool kApart = D == 64;
-  static constexpr int cP = kApart ? 384 : 0, kPStep = kApart ? 64 : 128;
+  static constexpr int cP = kApart ? 192 * TILES : 0, kPStep = kApart ? 64 : 128;
 };
 
 enum { bQ0 = 0, bQ1, bS0, bS1, bP0, bP1, bR0, bR1, bX0, bX1, bO0, bO1, bDone, bKV };  // then full / empty of every stage
 
 }  // namespace
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int TILES>
+__global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, FwdCfg<D, TILES>::kCtas)
     prompt_fwd_kernel(const __grid_constant__ PromptMaps maps, const PromptDev a) {
-  using C = FwdCfg<D>;
+  using C = FwdCfg<D, TILES>;
   constexpr int ST = C::kStages;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -85,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* status = reinterpret_cast<int*>(a.plan_dev);
   const PromptItem it = a.items[blockIdx.x];
   if (it.q0 < 0 || it.nq < 1 || it.k0 < 0 || it.lk < 0 || it.q0 + (long long)it.nq > a.Tq ||
-      it.k0 + (long long)it.lk > a.Tk || it.nq > a.tiles * a.tpt || it.b0 < 0 || it.head < 0) {
+      it.k0 + (long long)it.lk > a.Tk || it.nq > TILES * a.tpt || it.b0 < 0 || it.head < 0) {
     if (threadIdx.x == 0) atomicExch(status, kDevBadIndex);
     return;
   }
@@ -96,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long keys = a.causal ? min((long long)it.lk, (long long)it.pos0 + last + 1) : it.lk;
     return max(it.b0, min(it.b1, int((max(keys, 0LL) + 127) / 128)));
   };
-  const int nb0 = end_block(0), nb1 = end_block(1), bmax = max(nb0, nb1), n = bmax - it.b0;
+  const int nb0 = end_block(0), nb1 = TILES == 2 ? end_block(1) : it.b0, bmax = max(nb0, nb1), n = bmax - it.b0;
 
   volatile int* abort_flag = &abort_sh;
   auto bar = [&](int b) { return smem_u32(&bars[b]); };
@@ -117,7 +122,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < bKV + 2 * ST; ++i) mbar_init(bar(i), i >= bP0 && i <= bX1 ? 128 : 1);
     fence_barrier_init();
   }
-  if (warp == 9) tmem_alloc(smem_u32(&tmem_base_sh), 512);
+  asm volatile("griddepcontrol.launch_dependents;");  // the join's launch runs behind this kernel
+  if (warp == C::kSoft + 1) tmem_alloc(smem_u32(&tmem_base_sh), C::kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -131,11 +137,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // A row's 128 scores stay in its thread's registers: the softmax warps take
   // what the other four leave (2 x 232 + 40 = 3 x 168, the launch's own share).
-  if (warp == 8) {
-    reg_dec<40>();
+  if (warp == C::kSoft) {
+    if (TILES == 2) reg_dec<40>();
     if (lane == 0 && n > 0) {
       const int rows = a.G * a.tpt;
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < TILES; ++t) {
         if ((t == 0 ? nb0 : nb1) <= it.b0) continue;
         mbar_expect_tx(bar(bQ0 + t), rows * D * 2);
         for (int s = 0; s < D / 64; ++s)
@@ -160,8 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = max(0, issued - ST); i < issued; ++i) wait_drain(full(i), phase(i));
     }
     __syncwarp();
-  } else if (warp == 9) {
-    reg_dec<40>();
+  } else if (warp == C::kSoft + 1) {
+    if (TILES == 2) reg_dec<40>();
     constexpr uint32_t idS = idesc_bf16(128, 128, 0, 0);
     constexpr uint32_t idO = idesc_bf16(128, D, 0, 1);
     const int off[2] = {bmax - nb0, bmax - nb1};  // first step of each tile (n: none)
@@ -181,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (n > 0) {
       have_k(0);
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < TILES; ++t)
         if (off[t] == 0) issue_s(t, 0);
       mma_commit(bar(empty(0)));
     }
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (s + 1 < n) {
           have_k(s + 1);
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
+          for (int t = 0; t < TILES; ++t) {
             if (s >= off[t]) {  // S of this step has been read
               wait_w(bX0 + t, (s - off[t]) & 1);
               tc_fence_after();
@@ -234,13 +240,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         have_v();
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < TILES; ++t)
           if (s >= off[t]) issue_o(t);
       } else {
         have_v();
         bool have = false;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < TILES; ++t) {
           if (s >= off[t]) issue_o(t);
           if (s + 1 < n && s + 1 >= off[t]) {
             if (!have) have_k(s + 1);
@@ -255,8 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit(bar(bDone));
     wait_drain(bDone, 0);
     __syncwarp();
-  } else if (warp < 8) {
-    reg_inc<232>();
+  } else if (warp < C::kSoft) {
+    if (TILES == 2) reg_inc<232>();
     const int t = warp >> 2, r = threadIdx.x & 127;
     const int nb = t == 0 ? nb0 : nb1, steps = nb - it.b0;
     const int tok = t * a.tpt + r / a.G, g = r - (r / a.G) * a.G;
@@ -399,66 +405,88 @@ __global__ void __launch_bounds__(kThreads, 1)
         a.lse[token * a.Hq + head] = lse2 * 0.6931471805599453f;
     }
   } else {
-    reg_dec<40>();
+    reg_dec<40>();  // two tiles only: the idle warps
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == C::kSoft + 1) {
     tc_fence_after();
-    tmem_dealloc(tb, 512);
+    tmem_dealloc(tb, C::kCols);
   }
 }
 
 // Joins the partial results of rows whose keys were split: with L_i the parts'
 // log2-sums and M their maximum, O = sum 2^(L_i - M) O_i / sum 2^(L_i - M).
-// One warp per row, the parts in a fixed order. Bound: reading the parts.
+// One warp per row, the parts in a fixed order: the lanes fetch 32 parts' L at once,
+// and every part's O row is one 16-byte (d = 128) or 8-byte load per lane.
 template <int D>
 __global__ void __launch_bounds__(128) prompt_join_kernel(const PromptDev a) {
-  const PromptJoin jn = a.joins[blockIdx.x];
+  constexpr int V = D / 32;
+  const PromptJoin jn = a.joins[blockIdx.x];  // the plan's, written before the forward kernel began
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
   const int lane = threadIdx.x & 31;
   const int r = blockIdx.y * 4 + (threadIdx.x >> 5);
   const int t = r >> 7, rr = r & 127;
   const int tok = t * a.tpt + rr / a.G, g = rr - (rr / a.G) * a.G;
-  if (rr >= a.G * a.tpt || tok >= jn.nq) return;
+  if (rr >= a.G * a.tpt || tok >= jn.nq || jn.q0 + (long long)tok >= a.Tq) return;
   const size_t rows = size_t(a.tiles) * 128;
   float mx = -INFINITY;
-  for (int i = 0; i < jn.n; ++i) mx = max_nan(mx, a.part_lse[(jn.first + i) * rows + r]);
-  float o[D / 32], den = 0.0f;
+  for (int i = lane; i < jn.n; i += 32) mx = max_nan(mx, a.part_lse[(jn.first + i) * rows + r]);
+  for (int s = 16; s > 0; s >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+  float o[V], den = 0.0f;
 #pragma unroll
-  for (int x = 0; x < D / 32; ++x) o[x] = 0.0f;
-  if (mx != -INFINITY) {
-    for (int i = 0; i < jn.n; ++i) {
-      const size_t at = (jn.first + i) * rows + r;
-      const float w = exp2f(a.part_lse[at] - mx);
-      den += w;
+  for (int x = 0; x < V; ++x) o[x] = 0.0f;
+  for (int i0 = 0; i0 < jn.n && mx != -INFINITY; i0 += 32) {
+    const float w = i0 + lane < jn.n ? exp2f(a.part_lse[(jn.first + i0 + lane) * rows + r] - mx) : 0.0f;
+    const int end = min(32, jn.n - i0);
+#pragma unroll 4
+    for (int i = 0; i < end; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float* p = a.part + ((jn.first + i0 + i) * rows + r) * D + lane * V;
+      float x[V];
+      if (V == 4)
+        *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(p);
+      else
+        *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(p);
+      den += wi;
 #pragma unroll
-      for (int x = 0; x < D / 32; ++x) o[x] += w * a.part[at * D + lane * (D / 32) + x];
+      for (int y = 0; y < V; ++y) o[y] += wi * x[y];
     }
   }
   const float inv = den == 0.0f ? 0.0f : 1.0f / den;
   const long long token = (long long)jn.q0 + tok;
   const int head = jn.head * a.G + g;
-  __nv_bfloat16* orow = a.o + token * a.o_row + head * a.o_head + lane * (D / 32);
+  __nv_bfloat16* orow = a.o + token * a.o_row + head * a.o_head + lane * V;
 #pragma unroll
-  for (int x = 0; x < D / 32; x += 2) *reinterpret_cast<uint32_t*>(orow + x) = pack_bf16(o[x] * inv, o[x + 1] * inv);
+  for (int x = 0; x < V; x += 2) *reinterpret_cast<uint32_t*>(orow + x) = pack_bf16(o[x] * inv, o[x + 1] * inv);
   if (lane == 0 && a.lse)
     a.lse[token * a.Hq + head] = den == 0.0f ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
 }
 
 namespace {
 
-template <int D>
+template <int D, int TILES>
 cudaError_t set_up() {
-  return cudaFuncSetAttribute(prompt_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdCfg<D>::kSmem);
+  return cudaFuncSetAttribute(prompt_fwd_kernel<D, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              FwdCfg<D, TILES>::kSmem);
 }
 
-template <int D>
+template <int D, int TILES>
 cudaError_t launch_d(const PromptArgs& a, const PromptMaps& maps, const PromptDev& v, cudaStream_t s) {
-  prompt_fwd_kernel<D><<<a.plan->n_items, kThreads, FwdCfg<D>::kSmem, s>>>(maps, v);
+  using C = FwdCfg<D, TILES>;
+  prompt_fwd_kernel<D, TILES><<<a.plan->n_items, C::kThreads, C::kSmem, s>>>(maps, v);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.plan->n_joins == 0) return e;
-  prompt_join_kernel<D><<<dim3(a.plan->n_joins, a.plan->tiles * 32), 128, 0, s>>>(v);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.plan->n_joins, (a.plan->join_rows + 3) / 4);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prompt_join_kernel<D>, v);
 }
 
 }  // namespace
@@ -466,7 +494,8 @@ cudaError_t launch_d(const PromptArgs& a, const PromptMaps& maps, const PromptDe
 cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s) {
   const PromptPlan& p = *a.plan;
   // first, for it makes the device's context current in this thread, which the tensor maps need
-  const cudaError_t e = p.d == 128 ? set_up<128>() : set_up<64>();
+  const bool two = p.tiles == 2;
+  const cudaError_t e = p.d == 128 ? (two ? set_up<128, 2>() : set_up<128, 1>()) : (two ? set_up<64, 2>() : set_up<64, 1>());
   if (e != cudaSuccess) return e;
   PromptMaps maps;
   memset(&maps, 0, sizeof(maps));
@@ -492,7 +521,8 @@ cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s) {
   if (!map_queries(&maps.q, a.q, p.d, p.G, p.Hkv, p.Tq, v.tpt)) return cudaErrorInvalidValue;
   if (p.Tk > 0 && (!map_keys(&maps.k, a.k, p.d, p.Hkv, p.Tk) || !map_keys(&maps.v, a.v, p.d, p.Hkv, p.Tk)))
     return cudaErrorInvalidValue;
-  return p.d == 128 ? launch_d<128>(a, maps, v, s) : launch_d<64>(a, maps, v, s);
+  if (p.d == 128) return two ? launch_d<128, 2>(a, maps, v, s) : launch_d<128, 1>(a, maps, v, s);
+  return two ? launch_d<64, 2>(a, maps, v, s) : launch_d<64, 1>(a, maps, v, s);
 }
 
 }  // namespace sla
