@@ -387,11 +387,11 @@ sla_status sla_qk_norm_rope(const sla_heads* q, const sla_heads* k, const void* 
 size_t sla_qk_norm_rope_backward_workspace_size(int B, int N, int Hq, int Hk, int d);
 
 /* Gradients of <dyq, yq> + <dyk, yk>: dq, dk (rows n < N), and dwq, dwk ([d]
- * float32 device; both may be NULL). The norm is formed again from q and k.
+ * device, of the weights' type; both may be NULL; summed in float32). The norm is formed again from q and k.
  * workspace: 16-byte aligned device scratch. */
 sla_status sla_qk_norm_rope_backward(const sla_heads* q, const sla_heads* k, const void* wq, const void* wk,
                                      int w_f32, float eps, const sla_heads* dyq, const sla_heads* dyk,
-                                     const sla_heads* dq, const sla_heads* dk, float* dwq, float* dwk, int B, int N,
+                                     const sla_heads* dq, const sla_heads* dk, void* dwq, void* dwk, int B, int N,
                                      int d, int dtype, const sla_rope_spec* rope, void* workspace,
                                      size_t workspace_bytes, void* stream);
 

@@ -436,5 +436,20 @@ def attention(q, k, v, *, N: Optional[int] = None, variant: str = "sla", k_crit:
     return _SLAFunction.apply(q, k, v, w_proj, alpha)
 
 
-from .prompt import PromptPlan, prompt_attention, prompt_backward, prompt_forward, prompt_plan  # noqa: E402,F401
-from .rope import RopeTable, qk_norm_rope, qk_norm_rope_backward, rope, rope_table  # noqa: E402,F401
+# The operators beside the attention (modules rotary and prompt), loaded at their first use:
+# they import torch, which this module does not.
+_OPERATORS = {name: module for module, names in {
+    "rotary": ("RopeTable", "qk_norm_rope", "qk_norm_rope_backward", "rope", "rope_frequencies", "rope_table"),
+    "prompt": ("PromptPlan", "prompt_attention", "prompt_backward", "prompt_forward", "prompt_plan"),
+}.items() for name in names}
+
+
+def __getattr__(name):
+    module = _OPERATORS.get(name)
+    if module is None:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import importlib
+
+    value = getattr(importlib.import_module(f"{__name__}.{module}"), name)
+    globals()[name] = value
+    return value

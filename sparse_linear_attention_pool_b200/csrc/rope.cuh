@@ -9,7 +9,7 @@ namespace sla {
 struct RopeTensor {
   const void *x, *dy, *w;  // input; upstream gradient (backward); norm weight (null: no norm)
   void* y;                 // output (backward: dx)
-  float* dw;               // backward: [d] or null
+  void* dw;                // backward: [d] of the weights' type, or null
   long long xb, xn, xh, yb, yn, yh, gb, gn, gh;
   int H;
 };

@@ -167,7 +167,7 @@ size_t sla_qk_norm_rope_backward_workspace_size(int B, int N, int Hq, int Hk, in
 
 sla_status sla_qk_norm_rope_backward(const sla_heads* q, const sla_heads* k, const void* wq, const void* wk,
                                      int w_f32, float eps, const sla_heads* dyq, const sla_heads* dyk,
-                                     const sla_heads* dq, const sla_heads* dk, float* dwq, float* dwk, int B, int N,
+                                     const sla_heads* dq, const sla_heads* dk, void* dwq, void* dwk, int B, int N,
                                      int d, int dtype, const sla_rope_spec* rope, void* workspace,
                                      size_t workspace_bytes, void* stream) {
   sla_status st = check_sizes(B, N, d, dtype);
@@ -181,7 +181,9 @@ sla_status sla_qk_norm_rope_backward(const sla_heads* q, const sla_heads* k, con
   if (st == SLA_OK) st = check_weights(wq, wk, w_f32, eps, dtype);
   if (st != SLA_OK) return st;
   if ((dwq == nullptr) != (dwk == nullptr)) return SLA_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(dwq) % 4 != 0 || reinterpret_cast<uintptr_t>(dwk) % 4 != 0) return SLA_ERR_ALIGNMENT;
+  const size_t size = (w_f32 || dtype == SLA_FP32) ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(dwq) % size != 0 || reinterpret_cast<uintptr_t>(dwk) % size != 0)
+    return SLA_ERR_ALIGNMENT;
   if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 16 != 0 ||
       workspace_bytes < sla_qk_norm_rope_backward_workspace_size(B, N, q->H, k->H, d))
     return SLA_ERR_WORKSPACE;
@@ -192,7 +194,7 @@ sla_status sla_qk_norm_rope_backward(const sla_heads* q, const sla_heads* k, con
   a.w_f32 = w_f32 != 0 || dtype == SLA_FP32;
   const sla_heads *in[2] = {q, k}, *grad[2] = {dyq, dyk}, *out[2] = {dq, dk};
   const void* w[2] = {wq, wk};
-  float* dw[2] = {dwq, dwk};
+  void* dw[2] = {dwq, dwk};
   for (int i = 0; i < 2; ++i) {
     set_in(a.t[i], *in[i]);
     set_grad(a.t[i], *grad[i]);

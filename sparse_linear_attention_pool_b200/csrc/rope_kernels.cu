@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const RopeArgs 
 // column, then the slices. One block per 32 columns of one tensor.
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const RopeArgs a, int rows) {
   __shared__ float part[32][33];
-  float* dw = a.t[blockIdx.y].dw;
+  void* dw = a.t[blockIdx.y].dw;
   if (dw == nullptr) return;
   const int col = blockIdx.x * 32 + threadIdx.x % 32, slice = threadIdx.x / 32;
   float sum = 0.0f;
@@ -349,7 +349,12 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const RopeArgs a, int row
   if (slice == 0 && col < a.d) {
     float all = 0.0f;
     for (int k = 0; k < 32; ++k) all += part[k][threadIdx.x];
-    dw[col] = all;
+    if (a.w_f32)
+      static_cast<float*>(dw)[col] = all;
+    else if (a.dtype == SLA_BF16)
+      static_cast<__nv_bfloat16*>(dw)[col] = __float2bfloat16_rn(all);
+    else
+      static_cast<__half*>(dw)[col] = __float2half_rn(all);
   }
 }
 

@@ -16,6 +16,11 @@ from __future__ import annotations
 import ctypes
 from typing import Optional, Sequence
 
+import torch
+
+from . import PromptParams, Rows, SLAError, _check, load
+from .rotary import _on, current_stream
+
 
 class PromptPlan:
     """The work lists of a batch of sequences (see prompt_plan): host bytes and their device copy."""
@@ -26,16 +31,13 @@ class PromptPlan:
         self.Hq, self.Hkv, self.d, self.causal, self.grad = Hq, Hkv, d, causal, grad
         self.Tq, self.Tk = sum(self.lens_q), sum(self.lens_k)
         self.device = device_bytes.device
+        self._sizes = (self.Tq, self.Tk, Hq, Hkv, d)
         self._at = (ctypes.addressof(host), ctypes.sizeof(host), device_bytes.data_ptr())
-        from . import load
-
         self._workspace = load().sla_prompt_workspace_size(host)
         self._backward_workspace = load().sla_prompt_backward_workspace_size(host)
 
     def positions(self):
         """int32 [Tq] on the device: each query token's position in its sequence (for rope())."""
-        import torch
-
         return torch.cat([torch.arange(lk - lq, lk, dtype=torch.int32) for lq, lk in zip(self.lens_q, self.lens_k)]
                          ).to(self.device)
 
@@ -53,10 +55,6 @@ def prompt_plan(lens_q: Sequence[int], lens_k: Optional[Sequence[int]] = None, *
     the same lengths). Made once for a batch of lengths, and good for any number of calls.
     softmax_scale 0 selects 1 / sqrt(d). grad: whether the plan serves the backward pass too
     (default: for whole prompts, where lens_k is not given)."""
-    import torch
-
-    from . import PromptParams, SLAError, load
-
     lens_q = _lengths(lens_q, "lens_q")
     grad = lens_k is None if grad is None else bool(grad)
     lens_k = lens_q if lens_k is None else _lengths(lens_k, "lens_k")
@@ -81,149 +79,126 @@ def prompt_plan(lens_q: Sequence[int], lens_k: Optional[Sequence[int]] = None, *
                       int(Hq), int(Hkv), int(d), bool(causal), grad)
 
 
-def _rows(x, T: int, H: int, d: int, what: str):
-    """x as the kernels take it: rows of whole 16-byte pieces at 16-byte steps (copied where it is not)."""
-    import torch
-
-    if x.dtype != torch.bfloat16 or not x.is_cuda:
+def _rows(x, T: int, H: int, d: int, plan, what: str):
+    """(x, its sla_rows): rows of whole 16-byte pieces at 16-byte steps, copied where x's are not."""
+    if x.dtype is not torch.bfloat16 or not x.is_cuda:
         raise ValueError(f"{what}: a bfloat16 CUDA tensor")
-    if x.dim() != 3 or x.shape[1] != H or x.shape[2] != d or x.shape[0] < T:
-        raise ValueError(f"{what}: [>= {T}, {H}, {d}] for this plan, not {tuple(x.shape)}")
+    shape = x.shape
+    if len(shape) != 3 or shape[0] < T or shape[1] != H or shape[2] != d:
+        raise ValueError(f"{what}: [>= {T}, {H}, {d}] for this plan, not {tuple(shape)}")
+    if x.device != plan.device:
+        raise ValueError(f"{what}: on another device than the plan")
     row, head, one = x.stride()
     if one != 1 or (T > 1 and (row <= 0 or row % 8)) or (H > 1 and (head <= 0 or head % 8)) or x.data_ptr() % 16:
         x = x.contiguous()
-    return x
-
-
-def _struct(x):
-    from . import Rows
-
-    return Rows(x.data_ptr(), x.stride(0), x.stride(1))
-
-
-def _same_device(plan, *tensors):
-    for t in tensors:
-        if t.device != plan.device:
-            raise ValueError("the plan and the tensors are on different devices")
+        row, head, _ = x.stride()
+    return x, Rows(x.data_ptr(), row, head)
 
 
 def _out(x, out, T, H, d, what):
-    import torch
-
+    """(out, its sla_rows): a new tensor like x, or the given one."""
     if out is None:
-        return torch.empty((x.shape[0], H, d), dtype=x.dtype, device=x.device)
-    if out.dtype != x.dtype or out.device != x.device or out.dim() != 3 or out.shape[0] < T or \
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    elif out.dtype != x.dtype or out.device != x.device or out.dim() != 3 or out.shape[0] < T or \
             out.shape[1] != H or out.shape[2] != d or out.stride(2) != 1:
         raise ValueError(f"{what}: a [>= {T}, {H}, {d}] {x.dtype} tensor with contiguous rows")
-    return out
+    row, head, _ = out.stride()
+    return out, Rows(out.data_ptr(), row, head)
+
+
+def _forward(q, k, v, plan, out, want_lse, workspace):
+    Tq, Tk, Hq, Hkv, d = plan._sizes
+    q, q_rows = _rows(q, Tq, Hq, d, plan, "q")
+    k, k_rows = _rows(k, Tk, Hkv, d, plan, "k")
+    v, v_rows = _rows(v, Tk, Hkv, d, plan, "v")
+    out, o_rows = _out(q, out, Tq, Hq, d, "out")
+    lse = q.new_empty((Tq, Hq), dtype=torch.float32) if want_lse else None
+    if workspace is None and plan._workspace:
+        workspace = q.new_empty(plan._workspace, dtype=torch.uint8)
+    host, size, dev = plan._at
+    _check(load().sla_prompt_forward(
+        q_rows, k_rows, v_rows, o_rows, None if lse is None else lse.data_ptr(), host, size, dev,
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+        current_stream()), "sla_prompt_forward")
+    return out, lse
 
 
 def prompt_forward(q, k, v, plan: PromptPlan, *, out=None, want_lse: bool = True, workspace=None, stream=None):
     """(O, lse): sla_prompt_forward. O [rows of q, Hq, d]; lse [Tq, Hq] float32 or None.
     Rows of O behind the plan's last token are not written."""
-    import torch
-
-    from . import _check, load
-    from .rope import _on
-
     on = _on(q, stream)
     if on is not None:
         with on:
-            return prompt_forward(q, k, v, plan, out=out, want_lse=want_lse, workspace=workspace)
-    q, k, v = (_rows(q, plan.Tq, plan.Hq, plan.d, "q"), _rows(k, plan.Tk, plan.Hkv, plan.d, "k"),
-               _rows(v, plan.Tk, plan.Hkv, plan.d, "v"))
-    _same_device(plan, q, k, v)
-    out = _out(q, out, plan.Tq, plan.Hq, plan.d, "out")
-    lse = torch.empty((plan.Tq, plan.Hq), dtype=torch.float32, device=q.device) if want_lse else None
-    if workspace is None and plan._workspace:
-        workspace = torch.empty(plan._workspace, dtype=torch.uint8, device=q.device)
-    host, size, dev = plan._at
-    _check(load().sla_prompt_forward(
-        _struct(q), _struct(k), _struct(v), _struct(out), None if lse is None else lse.data_ptr(), host, size, dev,
-        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-        torch.cuda.current_stream().cuda_stream), "sla_prompt_forward")
-    return out, lse
+            return _forward(q, k, v, plan, out, want_lse, workspace)
+    return _forward(q, k, v, plan, out, want_lse, workspace)
 
 
-def prompt_backward(q, k, v, o, lse, do, plan: PromptPlan, *, out=None, workspace=None, stream=None):
-    """(dq, dk, dv): sla_prompt_backward for the upstream do of a prompt_forward's o and lse.
-    out: a triple of tensors to write to. Gradient rows behind the plan's last token are
-    zero, or with `out` as they were."""
-    import torch
-
-    from . import _check, load
-    from .rope import _on
-
-    on = _on(q, stream)
-    if on is not None:
-        with on:
-            return prompt_backward(q, k, v, o, lse, do, plan, out=out, workspace=workspace)
-    if not plan.grad:
-        raise ValueError("the plan was made without the backward pass (grad=True)")
-    Tq, Tk, Hq, Hkv, d = plan.Tq, plan.Tk, plan.Hq, plan.Hkv, plan.d
-    rows = (q.shape[0], k.shape[0])
-    q, k, v = _rows(q, Tq, Hq, d, "q"), _rows(k, Tk, Hkv, d, "k"), _rows(v, Tk, Hkv, d, "v")
-    o, do = _rows(o, Tq, Hq, d, "o"), _rows(do, Tq, Hq, d, "do")
-    _same_device(plan, q, k, v, o, do, lse)
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (Tq, Hq) or not lse.is_contiguous():
+def _backward(q, k, v, o, lse, do, plan, out, workspace):
+    Tq, Tk, Hq, Hkv, d = plan._sizes
+    q, q_rows = _rows(q, Tq, Hq, d, plan, "q")
+    k, k_rows = _rows(k, Tk, Hkv, d, plan, "k")
+    v, v_rows = _rows(v, Tk, Hkv, d, plan, "v")
+    o, o_rows = _rows(o, Tq, Hq, d, plan, "o")
+    do, do_rows = _rows(do, Tq, Hq, d, plan, "do")
+    if lse.dtype is not torch.float32 or tuple(lse.shape) != (Tq, Hq) or not lse.is_contiguous() or \
+            lse.device != plan.device:
         raise ValueError(f"lse: prompt_forward's [{Tq}, {Hq}] float32")
     dq, dk, dv = (None, None, None) if out is None else out
-    fresh = out is None
-    dq, dk, dv = _out(q, dq, Tq, Hq, d, "dq"), _out(k, dk, Tk, Hkv, d, "dk"), _out(v, dv, Tk, Hkv, d, "dv")
+    dq, dq_rows = _out(q, dq, Tq, Hq, d, "dq")
+    dk, dk_rows = _out(k, dk, Tk, Hkv, d, "dk")
+    dv, dv_rows = _out(v, dv, Tk, Hkv, d, "dv")
     if workspace is None:
-        workspace = torch.empty(plan._backward_workspace, dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(plan._backward_workspace, dtype=torch.uint8)
     host, size, dev = plan._at
     _check(load().sla_prompt_backward(
-        _struct(q), _struct(k), _struct(v), _struct(o), lse.data_ptr(), _struct(do), _struct(dq), _struct(dk),
-        _struct(dv), host, size, dev, workspace.data_ptr(), workspace.numel(),
-        torch.cuda.current_stream().cuda_stream), "sla_prompt_backward")
-    if fresh:
+        q_rows, k_rows, v_rows, o_rows, lse.data_ptr(), do_rows, dq_rows, dk_rows, dv_rows, host, size, dev,
+        workspace.data_ptr(), workspace.numel(), current_stream()), "sla_prompt_backward")
+    if out is None:
         for t, n in ((dq, Tq), (dk, Tk), (dv, Tk)):
             if t.shape[0] > n:
                 t[n:].zero_()
     return dq, dk, dv
 
 
-_function = None
+def _needs_backward(plan):
+    if not plan.grad:
+        raise ValueError("the plan was made without the backward pass (grad=True)")
 
 
-def _prompt_function():
-    """The autograd function (made at the first use: the package imports torch late)."""
-    global _function
-    if _function is not None:
-        return _function
-    import torch
+def prompt_backward(q, k, v, o, lse, do, plan: PromptPlan, *, out=None, workspace=None, stream=None):
+    """(dq, dk, dv): sla_prompt_backward for the upstream do of a prompt_forward's o and lse.
+    out: a triple of tensors to write to. Gradient rows behind the plan's last token are
+    zero, or with `out` as they were."""
+    _needs_backward(plan)
+    on = _on(q, stream)
+    if on is not None:
+        with on:
+            return _backward(q, k, v, o, lse, do, plan, out, workspace)
+    return _backward(q, k, v, o, lse, do, plan, out, workspace)
 
-    class PromptAttention(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, q, k, v, plan):
-            o, lse = prompt_forward(q, k, v, plan)
-            ctx.plan = plan
-            ctx.save_for_backward(q, k, v, o, lse)
-            return o
 
-        @staticmethod
-        @torch.autograd.function.once_differentiable
-        def backward(ctx, do):
-            return (*prompt_backward(*ctx.saved_tensors, do, ctx.plan), None)
+class _PromptAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, plan):
+        o, lse = _forward(q, k, v, plan, None, True, None)
+        ctx.plan = plan
+        ctx.save_for_backward(q, k, v, o, lse)
+        return o
 
-    _function = PromptAttention
-    return _function
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do):
+        return (*_backward(*ctx.saved_tensors, do, ctx.plan, None, None), None)
 
 
 def prompt_attention(q, k, v, plan: PromptPlan, *, stream=None):
     """O = softmax(scale Q K^T + mask) V for the plan's packed sequences, [rows of q, Hq, d].
     Differentiable in q, k and v (with a plan made for it)."""
-    import torch
-
-    from .rope import _on
-
     on = _on(q, stream)
     if on is not None:
         with on:
             return prompt_attention(q, k, v, plan)
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
-        if not plan.grad:
-            raise ValueError("the plan was made without the backward pass (grad=True)")
-        return _prompt_function().apply(q, k, v, plan)
-    return prompt_forward(q, k, v, plan, want_lse=False)[0]
+        _needs_backward(plan)
+        return _PromptAttention.apply(q, k, v, plan)
+    return _forward(q, k, v, plan, None, False, None)[0]

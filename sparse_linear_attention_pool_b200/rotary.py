@@ -12,9 +12,12 @@ logical shape. Both calls are differentiable: in the inputs and the weights.
 """
 from __future__ import annotations
 
-import ctypes
 import math
 from typing import Optional, Sequence
+
+import torch
+
+from . import Heads, RopeSpec, _check, load
 
 LAYOUTS = {"interleaved": 0, "half": 1}
 SCALINGS = ("none", "linear", "ntk", "yarn")
@@ -86,8 +89,6 @@ def rope_table(rot_dim: int, *, layout: str = "interleaved", freqs: Optional[Seq
     layout "interleaved": pair i is (x[2i], x[2i+1]); "half": (x[i], x[i + rot_dim/2]).
     The other arguments are rope_frequencies'; `freqs` (radians per position, rot_dim / 2
     numbers, in place of theta and the scaling) and `gain` set them directly."""
-    import torch
-
     if layout not in LAYOUTS:
         raise ValueError(f"layout must be one of {tuple(LAYOUTS)}")
     if freqs is not None:
@@ -114,13 +115,15 @@ def rope_table(rot_dim: int, *, layout: str = "interleaved", freqs: Optional[Seq
                      tuple(made))
 
 
-def _dtype_code(x) -> int:
-    import torch
+_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the current stream's handle, without an object
 
-    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(x.dtype)
-    if code is None:
-        raise ValueError(f"bfloat16, float16 or float32 tensors, not {x.dtype}")
-    return code
+
+def current_stream() -> int:
+    """The current device's current stream as an integer handle."""
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _check_rows(x, like=None, what="x"):
@@ -128,6 +131,8 @@ def _check_rows(x, like=None, what="x"):
         raise ValueError(f"{what}: [B, H, N, d] or [T, H, d], not {tuple(x.shape)}")
     if not x.is_cuda:
         raise ValueError(f"{what}: a CUDA tensor")
+    if x.dtype not in _CODES:
+        raise ValueError(f"{what}: bfloat16, float16 or float32, not {x.dtype}")
     if like is not None and (x.dim() != like.dim() or x.dtype != like.dtype or x.device != like.device
                              or x.shape[-1] != like.shape[-1]):
         raise ValueError(f"{what}: dtype, device, head size or rank differ")
@@ -139,8 +144,6 @@ def _rows(x):
 
 
 def _heads(x):
-    from . import Heads
-
     if x.dim() == 4:
         sb, sh, sn, _ = x.stride()
         return Heads(x.data_ptr(), x.shape[1], sb, sh, sn)
@@ -154,60 +157,54 @@ def _tokens(x):
 
 def _spec(table: Optional[RopeTable], positions, B: int, N: int, device):
     """The sla_rope_spec of a call, positions checked against B and N."""
-    from . import RopeSpec
-
     if table is None:
         if positions is not None:
             raise ValueError("positions without a table")
         return None
     if table.device != device:
         raise ValueError("the table is on another device")
+    turns, axis = table._fixed
+    gain, rot_dim, layout, n_axes = table._tail
     if positions is None:
-        return RopeSpec(*table._fixed, None, 0, 0, 0, table._tail[0], 32, *table._tail[1:])
-    import torch
-
-    if positions.dtype not in (torch.int32, torch.int64) or positions.device != device:
+        return RopeSpec(turns, axis, None, 0, 0, 0, gain, 32, rot_dim, layout, n_axes)
+    bits = 32 if positions.dtype is torch.int32 else 64
+    if (bits == 64 and positions.dtype is not torch.int64) or positions.device != device:
         raise ValueError("positions: int32 or int64 on the tensors' device")
-    shape, stride = list(positions.shape), list(positions.stride())
-    s_axis = 0
-    if table.n_axes > 1:
-        if len(shape) < 2 or shape[0] != table.n_axes:
-            raise ValueError(f"positions: [{table.n_axes}, (B,) N] for {table.n_axes} axes")
-        s_axis = stride[0]
-        shape, stride = shape[1:], stride[1:]
-    if len(shape) not in (1, 2) or shape[-1] < N or (len(shape) == 2 and shape[0] not in (1, B)):
+    shape, stride, s_axis, s_b = positions.shape, positions.stride(), 0, 0
+    if n_axes > 1:
+        if len(shape) < 2 or shape[0] != n_axes:
+            raise ValueError(f"positions: [{n_axes}, (B,) N] for {n_axes} axes")
+        s_axis, shape, stride = stride[0], shape[1:], stride[1:]
+    if len(shape) == 2 and shape[0] in (1, B):
+        s_b = stride[0] if shape[0] > 1 else 0
+    elif len(shape) != 1:
+        shape = (-1,)
+    if shape[-1] < N:
         raise ValueError(f"positions: one for each of {B} x {N} tokens, not {tuple(positions.shape)}")
-    s_b = stride[0] if len(shape) == 2 and shape[0] > 1 else 0
-    return RopeSpec(*table._fixed, positions.data_ptr(), s_axis, s_b, stride[-1], table._tail[0],
-                    32 if positions.dtype == torch.int32 else 64, *table._tail[1:])
+    return RopeSpec(turns, axis, positions.data_ptr(), s_axis, s_b, stride[-1], gain, bits, rot_dim, layout, n_axes)
 
 
 def _on(x, stream):
     """A context that makes x's device current and `stream` its current stream, or None."""
-    import torch
-
     if stream is not None:
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=x.device)
         return torch.cuda.stream(stream)
-    if x.is_cuda and x.device.index != torch.cuda.current_device():
+    if x.is_cuda and x.get_device() != torch.cuda.current_device():
         return torch.cuda.device(x.device)
     return None
 
 
 def _out_for(x, out, rows: Optional[int], N: int, what="out"):
-    import torch
-
     if out is None:
-        if x.dim() == 4:
-            B, H, n, d = x.shape
-            rows = n if rows is None else int(rows)
-            if rows < N:
-                raise ValueError("rows must be at least N")
-            return torch.empty((B, H, rows, d), dtype=x.dtype, device=x.device)
-        if rows is not None:
+        if rows is None:
+            return torch.empty_like(x, memory_format=torch.contiguous_format)
+        if x.dim() != 4:
             raise ValueError("rows is for [B, H, N, d] tensors")
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        B, H, _, d = x.shape
+        if int(rows) < N:
+            raise ValueError("rows must be at least N")
+        return x.new_empty((B, H, int(rows), d))
     _check_rows(out, x, what)
     if out.shape[1] != x.shape[1] or (out.dim() == 4 and out.shape[0] != x.shape[0]) or _tokens(out)[1] < N:
         raise ValueError(f"{what}: shape {tuple(out.shape)} does not take the result")
@@ -226,15 +223,11 @@ def _count(x, N):
 
 
 def _run_rope(x, table, positions, N, out, inverse):
-    from . import _check, load
-    import torch
-
-    B = _tokens(x)[0]
+    B = x.shape[0] if x.dim() == 4 else 1
     spec = _spec(table, positions, B, N, x.device)
-    if B and N and x.shape[1] and x.shape[-1]:
-        hx, hy = _heads(x), _heads(out)
-        _check(load().sla_rope(hx, hy, B, N, x.shape[-1], _dtype_code(x), spec, int(inverse),
-                               torch.cuda.current_stream().cuda_stream), "sla_rope")
+    if N and x.numel():
+        _check(load().sla_rope(_heads(x), _heads(out), B, N, x.shape[-1], _CODES[x.dtype], spec, int(inverse),
+                               current_stream()), "sla_rope")
     return out
 
 
@@ -245,56 +238,41 @@ def _zero_tail(t, N):
     return t
 
 
-_classes = None
+class _Rope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, table, positions, N, rows, inverse):
+        ctx.save_for_backward(positions)
+        ctx.meta = (table, N, inverse, x.shape)
+        x = _rows(x)
+        return _run_rope(x, table, positions, N, _out_for(x, None, rows, N), inverse)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        table, N, inverse, shape = ctx.meta
+        (positions,) = ctx.saved_tensors
+        dx = torch.empty(shape, dtype=dy.dtype, device=dy.device)
+        _run_rope(_rows(dy), table, positions, N, dx, not inverse)
+        return _zero_tail(dx, N), None, None, None, None, None
 
 
-def _functions():
-    """The autograd functions (made at the first use: the package imports torch late)."""
-    global _classes
-    if _classes is not None:
-        return _classes
-    import torch
+class _QKNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, wq, wk, table, positions, eps, N, rows):
+        ctx.meta = (table, eps, N)
+        ctx.save_for_backward(q, k, wq, wk, positions)
+        q, k = _rows(q), _rows(k)
+        return _run_norm(q, k, wq, wk, table, positions, eps, N, _out_for(q, None, rows, N),
+                         _out_for(k, None, rows, N))
 
-    class Rope(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, x, table, positions, N, rows, inverse):
-            ctx.save_for_backward(positions)
-            ctx.meta = (table, N, inverse, x.shape)
-            x = _rows(x)
-            return _run_rope(x, table, positions, N, _out_for(x, None, rows, N), inverse)
-
-        @staticmethod
-        @torch.autograd.function.once_differentiable
-        def backward(ctx, dy):
-            table, N, inverse, shape = ctx.meta
-            (positions,) = ctx.saved_tensors
-            dx = torch.empty(shape, dtype=dy.dtype, device=dy.device)
-            _run_rope(_rows(dy), table, positions, N, dx, not inverse)
-            return _zero_tail(dx, N), None, None, None, None, None
-
-    class QKNormRope(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, q, k, wq, wk, table, positions, eps, N, rows):
-            ctx.meta = (table, eps, N)
-            ctx.save_for_backward(q, k, wq, wk, positions)
-            q, k = _rows(q), _rows(k)
-            return _run_norm(q, k, wq, wk, table, positions, eps, N, _out_for(q, None, rows, N),
-                             _out_for(k, None, rows, N))
-
-        @staticmethod
-        @torch.autograd.function.once_differentiable
-        def backward(ctx, dyq, dyk):
-            q, k, wq, wk, positions = ctx.saved_tensors
-            table, eps, N = ctx.meta
-            need_w = ctx.needs_input_grad[2] or ctx.needs_input_grad[3]
-            dq, dk, dwq, dwk = qk_norm_rope_backward(q, k, wq, wk, dyq, dyk, table, positions, eps=eps, N=N,
-                                                     want_weight_grad=need_w)
-            if need_w:
-                dwq, dwk = dwq.to(wq.dtype), dwk.to(wk.dtype)
-            return dq, dk, dwq, dwk, None, None, None, None, None
-
-    _classes = (Rope, QKNormRope)
-    return _classes
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dyq, dyk):
+        q, k, wq, wk, positions = ctx.saved_tensors
+        table, eps, N = ctx.meta
+        need_w = ctx.needs_input_grad[2] or ctx.needs_input_grad[3]
+        return (*_run_norm_backward(q, k, wq, wk, dyq, dyk, table, positions, eps, N, need_w, None),
+                None, None, None, None, None)
 
 
 def rope(x, table: RopeTable, positions=None, *, N: Optional[int] = None, rows: Optional[int] = None, out=None,
@@ -306,8 +284,6 @@ def rope(x, table: RopeTable, positions=None, *, N: Optional[int] = None, rows: 
     a [B, H, n, d] tensor are taken; `rows` (>= N) is the length of the result, whose rows
     behind N are not written. out: a tensor to write to (x itself is allowed).
     inverse rotates back by the same angles."""
-    import torch
-
     on = _on(x, stream)
     if on is not None:
         with on:
@@ -317,7 +293,7 @@ def rope(x, table: RopeTable, positions=None, *, N: Optional[int] = None, rows: 
     if torch.is_grad_enabled() and x.requires_grad:
         if out is not None:
             raise ValueError("out cannot be given for a tensor that requires grad")
-        return _functions()[0].apply(x, table, positions, N, rows, inverse)
+        return _Rope.apply(x, table, positions, N, rows, inverse)
     x = _rows(x)
     return _run_rope(x, table, positions, N, _out_for(x, out, rows, N), inverse)
 
@@ -330,8 +306,6 @@ def _check_pair(q, k, wq, wk):
     for w, what in ((wq, "wq"), (wk, "wk")):
         if w.dim() != 1 or w.shape[0] != q.shape[-1] or w.device != q.device:
             raise ValueError(f"{what}: [d] on the tensors' device")
-    import torch
-
     if wq.dtype != wk.dtype or wq.dtype not in (q.dtype, torch.float32):
         raise ValueError("wq and wk: the tensors' dtype, or float32")
 
@@ -341,16 +315,13 @@ def _weight(w):
 
 
 def _run_norm(q, k, wq, wk, table, positions, eps, N, yq, yk):
-    from . import _check, load
-    import torch
-
     B = _tokens(q)[0]
     spec = _spec(table, positions, B, N, q.device)
     if B and N:
         wq, wk = _weight(wq), _weight(wk)
         _check(load().sla_qk_norm_rope(_heads(q), _heads(k), wq.data_ptr(), wk.data_ptr(),
                                        int(wq.dtype == torch.float32), eps, _heads(yq), _heads(yk), B, N,
-                                       q.shape[-1], _dtype_code(q), spec, torch.cuda.current_stream().cuda_stream),
+                                       q.shape[-1], _CODES[q.dtype], spec, current_stream()),
                "sla_qk_norm_rope")
     return yq, yk
 
@@ -363,8 +334,6 @@ def qk_norm_rope(q, k, wq, wk, table: Optional[RopeTable] = None, positions=None
     wq, wk: [d], of the tensors' dtype or float32. table None: the norm alone.
     q and k may have different numbers of heads. The other arguments are rope()'s;
     out: a pair of tensors."""
-    import torch
-
     on = _on(q, stream)
     if on is not None:
         with on:
@@ -374,23 +343,41 @@ def qk_norm_rope(q, k, wq, wk, table: Optional[RopeTable] = None, positions=None
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or wq.requires_grad or wk.requires_grad):
         if out is not None:
             raise ValueError("out cannot be given for tensors that require grad")
-        return _functions()[1].apply(q, k, wq, wk, table, positions, float(eps), N, rows)
+        return _QKNormRope.apply(q, k, wq, wk, table, positions, float(eps), N, rows)
     q, k = _rows(q), _rows(k)
     yq, yk = (None, None) if out is None else out
     return _run_norm(q, k, wq, wk, table, positions, eps, N, _out_for(q, yq, rows, N),
                      _out_for(k, yk, rows, N, "out"))
 
 
+def _run_norm_backward(q, k, wq, wk, dyq, dyk, table, positions, eps, N, need_w, workspace):
+    B, d = _tokens(q)[0], q.shape[-1]
+    dq, dk = (torch.empty_like(x, memory_format=torch.contiguous_format) for x in (q, k))
+    dwq, dwk = (torch.empty_like(wq), torch.empty_like(wk)) if need_w else (None, None)
+    spec = _spec(table, positions, B, N, q.device)
+    if B and N:
+        lib = load()
+        if workspace is None:
+            workspace = q.new_empty(lib.sla_qk_norm_rope_backward_workspace_size(B, N, q.shape[1], k.shape[1], d),
+                                    dtype=torch.uint8)
+        q, k, dyq, dyk, wq, wk = _rows(q), _rows(k), _rows(dyq), _rows(dyk), _weight(wq), _weight(wk)
+        _check(lib.sla_qk_norm_rope_backward(
+            _heads(q), _heads(k), wq.data_ptr(), wk.data_ptr(), int(wq.dtype == torch.float32), eps, _heads(dyq),
+            _heads(dyk), _heads(dq), _heads(dk), dwq.data_ptr() if need_w else None,
+            dwk.data_ptr() if need_w else None, B, N, d, _CODES[q.dtype], spec, workspace.data_ptr(),
+            workspace.numel(), current_stream()), "sla_qk_norm_rope_backward")
+    elif need_w:
+        dwq.zero_()
+        dwk.zero_()
+    return _zero_tail(dq, N), _zero_tail(dk, N), dwq, dwk
+
+
 def qk_norm_rope_backward(q, k, wq, wk, dyq, dyk, table: Optional[RopeTable] = None, positions=None, *,
                           eps: float = 1e-6, N: Optional[int] = None, want_weight_grad: bool = True,
                           workspace=None, stream=None):
     """Gradients (dq, dk, dwq, dwk) of qk_norm_rope for the upstream dyq, dyk
-    (sla_qk_norm_rope_backward); dwq, dwk float32 [d] or None. Rows behind N of dq and
-    dk are zero, those of dyq and dyk are not read."""
-    import torch
-
-    from . import _check, load
-
+    (sla_qk_norm_rope_backward); dwq, dwk of the weights' dtype, or None. Rows behind N
+    of dq and dk are zero, those of dyq and dyk are not read."""
     on = _on(q, stream)
     if on is not None:
         with on:
@@ -402,22 +389,4 @@ def qk_norm_rope_backward(q, k, wq, wk, dyq, dyk, table: Optional[RopeTable] = N
         _check_rows(g, x, what)
         if g.shape[1] != x.shape[1] or _tokens(g)[0] != _tokens(x)[0] or _tokens(g)[1] < N:
             raise ValueError(f"{what}: shape {tuple(g.shape)}")
-    B, d = _tokens(q)[0], q.shape[-1]
-    dq, dk = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
-    dw = torch.empty((2, d), dtype=torch.float32, device=q.device) if want_weight_grad else None
-    spec = _spec(table, positions, B, N, q.device)
-    if B and N:
-        lib = load()
-        need = lib.sla_qk_norm_rope_backward_workspace_size(B, N, q.shape[1], k.shape[1], d)
-        if workspace is None:
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        q, k, dyq, dyk, wq, wk = _rows(q), _rows(k), _rows(dyq), _rows(dyk), _weight(wq), _weight(wk)
-        at = None if dw is None else dw.data_ptr()
-        _check(lib.sla_qk_norm_rope_backward(
-            _heads(q), _heads(k), wq.data_ptr(), wk.data_ptr(), int(wq.dtype == torch.float32), eps, _heads(dyq),
-            _heads(dyk), _heads(dq), _heads(dk), at, None if at is None else at + 4 * d, B, N, d, _dtype_code(q),
-            spec, workspace.data_ptr(), workspace.numel(), torch.cuda.current_stream().cuda_stream),
-            "sla_qk_norm_rope_backward")
-    elif dw is not None:
-        dw.zero_()
-    return _zero_tail(dq, N), _zero_tail(dk, N), None if dw is None else dw[0], None if dw is None else dw[1]
+    return _run_norm_backward(q, k, wq, wk, dyq, dyk, table, positions, float(eps), N, want_weight_grad, workspace)

@@ -10,7 +10,7 @@ import torch
 
 import sparse_linear_attention_pool_b200 as sla
 from sparse_linear_attention_pool_b200 import build as sla_build
-from sparse_linear_attention_pool_b200.rope import rope_frequencies
+from sparse_linear_attention_pool_b200.rotary import rope_frequencies
 from tests import operator_reference as R
 
 
@@ -158,7 +158,7 @@ def test_backward_workspace(lib):
     assert call(0x100008, 1 << 30) == sla.SLA_ERR_WORKSPACE
     assert call(0x100000, small - 1) == sla.SLA_ERR_WORKSPACE
     assert call(0x100000, 1 << 30, dwq=0x4000) == sla.SLA_ERR_INVALID_ARG
-    assert call(0x100000, 1 << 30, dwq=0x4002, dwk=0x4000) == sla.SLA_ERR_ALIGNMENT
+    assert call(0x100000, 1 << 30, dwq=0x4001, dwk=0x4000) == sla.SLA_ERR_ALIGNMENT
     assert call(0x100000, 1 << 30, dyq=heads(H=3)) == sla.SLA_ERR_INVALID_ARG
 
 

@@ -68,7 +68,7 @@ def positions_of(axes, B, N, seed, form):
 
 def reference_angles(table, pos, axes, B, N):
     """[B][N, pairs]"""
-    from sparse_linear_attention_pool_b200.rope import RopeTable  # noqa: F401
+    from sparse_linear_attention_pool_b200.rotary import RopeTable  # noqa: F401
 
     axis = None if table.axis is None else table.axis.cpu().tolist()
     out = []
