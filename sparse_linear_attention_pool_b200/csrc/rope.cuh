@@ -23,12 +23,13 @@ struct RopeArgs {
   int pos64, n_axes;
   long long pos_axis, pos_b, pos_n;
   float gain, eps, inv_d;
-  float* partial;  // backward: [tensors][blocks][d]
-  int tpr, hpg;    // lanes per head row, heads per lane group (set by the launcher)
+  float* partial;  // backward: [blocks][d]
+  // set by the launcher: lanes per head row, heads per lane group; backward: blocks of q, the rest are k's
+  int tpr, hpg, split;
 };
 
-constexpr int kRopeBwdBlocks = 148 * 4;
-int rope_bwd_blocks(long long tokens, int heads);
+constexpr int kRopeBwdBlocks = 148 * 3;
+int rope_bwd_blocks(long long tokens);
 // Forward (rotation, or norm and rotation where t[i].w is set) or, with bwd, the norm's backward.
 cudaError_t launch_rope(RopeArgs a, int tensors, bool bwd, cudaStream_t s);
 

@@ -162,7 +162,7 @@ sla_status sla_qk_norm_rope(const sla_heads* q, const sla_heads* k, const void* 
 
 size_t sla_qk_norm_rope_backward_workspace_size(int B, int N, int Hq, int Hk, int d) {
   if (check_sizes(B, N, d, SLA_BF16) != SLA_OK || Hq < 1 || Hk < 1 || Hq > 65535 || Hk > 65535) return 0;
-  return size_t(2) * rope_bwd_blocks((long long)B * N, std::max(Hq, Hk)) * d * sizeof(float);
+  return size_t(rope_bwd_blocks((long long)B * N)) * d * sizeof(float);
 }
 
 sla_status sla_qk_norm_rope_backward(const sla_heads* q, const sla_heads* k, const void* wq, const void* wk,

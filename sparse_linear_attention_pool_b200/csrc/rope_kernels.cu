@@ -13,12 +13,14 @@
 //
 // Bound: HBM (each value read and written once). Split: `tpr` lanes share a
 // head row, each with one unit = two chunks of V values that hold V whole pairs
-// (layout "half": chunks V apart by rot / 2; "interleaved": two neighbours), so
-// no value crosses a lane; only the norm's sum does, by shuffles. A lane keeps
-// its V cos / sin pairs in registers and walks over the heads of its token, so
-// the sines (about 40 instructions each) are paid once per token and not per
-// head. Neighbouring lane groups take neighbouring tokens: a head-major output
-// is then written in runs of whole tiles.
+// (layout "half": chunks rot / 2 apart; "interleaved": two neighbours), so no
+// value crosses a lane; only the norm's sum does, by shuffles. A lane keeps its
+// V cos / sin pairs in registers and walks over the heads of its token, so the
+// sines are paid once per token and not per head.
+// The next heads' chunks are on their way meanwhile, as they came from memory.
+// V = 4: chunks of 8 as 16-byte loads held twice the registers, a third of the
+// warps and 3.9 TB/s. Neighbouring lane groups take neighbouring tokens: a
+// head-major output is then written in runs of whole tiles.
 #include "sla_internal.cuh"
 
 #include <cuda_fp16.h>
@@ -31,22 +33,12 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T>
-__device__ __forceinline__ float to_f(T x);
-template <>
 __device__ __forceinline__ float to_f(float x) { return x; }
-template <>
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <>
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-template <typename T>
-__device__ __forceinline__ T from_f(float x);
-template <>
-__device__ __forceinline__ float from_f(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
-template <>
-__device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
+__device__ __forceinline__ void from_f(float x, float& y) { y = x; }
+__device__ __forceinline__ void from_f(float x, __nv_bfloat16& y) { y = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void from_f(float x, __half& y) { y = __float2half_rn(x); }
 
 // V values in one access of V * sizeof(T) bytes
 template <typename T, int V>
@@ -54,8 +46,11 @@ struct alignas(V * sizeof(T)) Chunk {
   T e[V];
 };
 template <typename T, int V>
-__device__ __forceinline__ void load_chunk(const T* p, float (&f)[V]) {
-  const Chunk<T, V> c = *reinterpret_cast<const Chunk<T, V>*>(p);
+__device__ __forceinline__ Chunk<T, V> fetch_chunk(const T* p) {
+  return *reinterpret_cast<const Chunk<T, V>*>(p);
+}
+template <typename T, int V>
+__device__ __forceinline__ void widen(const Chunk<T, V>& c, float (&f)[V]) {
 #pragma unroll
   for (int j = 0; j < V; ++j) f[j] = to_f(c.e[j]);
 }
@@ -63,8 +58,43 @@ template <typename T, int V>
 __device__ __forceinline__ void store_chunk(T* p, const float (&f)[V]) {
   Chunk<T, V> c;
 #pragma unroll
-  for (int j = 0; j < V; ++j) c.e[j] = from_f<T>(f[j]);
+  for (int j = 0; j < V; ++j) from_f(f[j], c.e[j]);
   *reinterpret_cast<Chunk<T, V>*>(p) = c;
+}
+// four 16-bit values: two 32-bit words, converted in pairs
+template <typename T>
+struct alignas(8) Chunk4 {
+  uint32_t w[2];
+};
+template <>
+struct Chunk<__nv_bfloat16, 4> : Chunk4<__nv_bfloat16> {};
+template <>
+struct Chunk<__half, 4> : Chunk4<__half> {};
+__device__ __forceinline__ void widen(const Chunk<__nv_bfloat16, 4>& c, float (&f)[4]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    f[2 * j] = bf16_lo(c.w[j]);
+    f[2 * j + 1] = bf16_hi(c.w[j]);
+  }
+}
+__device__ __forceinline__ void widen(const Chunk<__half, 4>& c, float (&f)[4]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&c.w[j]));
+    f[2 * j] = v.x;
+    f[2 * j + 1] = v.y;
+  }
+}
+__device__ __forceinline__ uint32_t narrow2(float a, float b, const __nv_bfloat16*) { return pack_bf16(a, b); }
+__device__ __forceinline__ uint32_t narrow2(float a, float b, const __half*) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void store_chunk(__nv_bfloat16* p, const float (&f)[4]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(narrow2(f[0], f[1], p), narrow2(f[2], f[3], p));
+}
+__device__ __forceinline__ void store_chunk(__half* p, const float (&f)[4]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(narrow2(f[0], f[1], p), narrow2(f[2], f[3], p));
 }
 
 // The two chunks (element offsets) of unit u; unit u holds pairs u V .. u V + V - 1 while u V < rot / 2.
@@ -79,30 +109,28 @@ __device__ __forceinline__ void unit_offsets(int u, int rot, int& ea, int& eb) {
   }
 }
 
-// (a, b) of one unit turned by (c, s): across the chunks, or (V > 1, interleaved) inside them
+// The two values of pair j of a unit's chunks: across them, or (V > 1, interleaved) inside them
+template <int V, bool HALF>
+__device__ __forceinline__ float& first(float (&a)[V], float (&b)[V], int j) {
+  return HALF || V == 1 ? a[j] : j < V / 2 ? a[2 * j] : b[2 * j - V];
+}
+template <int V, bool HALF>
+__device__ __forceinline__ float& second(float (&a)[V], float (&b)[V], int j) {
+  return HALF || V == 1 ? b[j] : j < V / 2 ? a[2 * j + 1] : b[2 * j - V + 1];
+}
+// (u, v) -> (u c - v s, v c + u s); the operations are spelled out, so that every chunk width rounds alike
 template <int V, bool HALF>
 __device__ __forceinline__ void rotate(float (&a)[V], float (&b)[V], const float (&c)[V], const float (&s)[V]) {
-  if (HALF || V == 1) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float u = a[j], v = b[j];
-      a[j] = u * c[j] - v * s[j];
-      b[j] = v * c[j] + u * s[j];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < V / 2; ++j) {
-      const float u = a[2 * j], v = a[2 * j + 1];
-      a[2 * j] = u * c[j] - v * s[j];
-      a[2 * j + 1] = v * c[j] + u * s[j];
-      const float x = b[2 * j], y = b[2 * j + 1];
-      b[2 * j] = x * c[V / 2 + j] - y * s[V / 2 + j];
-      b[2 * j + 1] = y * c[V / 2 + j] + x * s[V / 2 + j];
-    }
+  for (int j = 0; j < V; ++j) {
+    float &u = first<V, HALF>(a, b, j), &v = second<V, HALF>(a, b, j);
+    const float x = fmaf(u, c[j], -__fmul_rn(v, s[j]));
+    v = fmaf(v, c[j], __fmul_rn(u, s[j]));
+    u = x;
   }
 }
 
-template <int V>
+template <typename T, int V>
 __device__ __forceinline__ void angles(const RopeArgs& a, int b, int n, int u, float (&c)[V], float (&s)[V]) {
   long long p = n;
   auto position = [&](int axis) {
@@ -122,15 +150,31 @@ __device__ __forceinline__ void angles(const RopeArgs& a, int b, int n, int u, f
     const unsigned long long turn = a.turns[i] * static_cast<unsigned long long>(p);
     const float half_turns = float(int(turn >> 32)) * 0x1p-31f;  // in [-1, 1]
     float sn, cs;
-    sincospif(half_turns, &sn, &cs);
+    if (sizeof(T) == 2) {
+      // off by 2^-20.5 at most within +-pi: a five-hundredth of an fp16 half-step, at a tenth of the instructions
+      __sincosf(half_turns * 3.14159265358979f, &sn, &cs);
+    } else {
+      sincospif(half_turns, &sn, &cs);
+    }
     c[j] = cs * a.gain;
     s[j] = a.inverse ? -sn * a.gain : sn * a.gain;
   }
 }
 
 __device__ __forceinline__ float group_sum(float x, int tpr) {
-  for (int o = tpr >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < tpr) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
+}
+__device__ __forceinline__ void group_sum2(float& x, float& y, int tpr) {  // two chains at once
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < tpr) {
+      const float p = __shfl_xor_sync(0xffffffffu, x, o), q = __shfl_xor_sync(0xffffffffu, y, o);
+      x += p;
+      y += q;
+    }
 }
 
 template <int V>
@@ -155,15 +199,13 @@ __device__ __forceinline__ void load_weight(const RopeArgs& a, const void* w, in
 
 // grid: (token tiles, tensors, head ranges). NU units per lane (1 but for V = 1).
 template <typename T, int V, int NU, bool HALF, bool NORM>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, NU == 1 ? 4 : 2) rope_kernel(const RopeArgs a) {
   const RopeTensor& t = a.t[blockIdx.y];
   const int lane = threadIdx.x % a.tpr, group = threadIdx.x / a.tpr;
   const unsigned tok = blockIdx.x * unsigned(kThreads / a.tpr) + group;
   const int h0 = blockIdx.z * a.hpg, h1 = min(t.H, h0 + a.hpg);
   const bool live = tok < unsigned(a.B) * unsigned(a.N);
   const int b = live ? int(tok / unsigned(a.N)) : 0, n = live ? int(tok - unsigned(b) * unsigned(a.N)) : 0;
-  float c[NU][V], s[NU][V];
-  float wa[NORM ? NU : 1][V], wb[NORM ? NU : 1][V];
   int ea[NU], eb[NU];
   bool on[NU];
 #pragma unroll
@@ -172,70 +214,91 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
     on[k] = live && 2 * u * V < a.d;
     unit_offsets<V, HALF>(u, a.rot, ea[k], eb[k]);
   }
-  const T* x = static_cast<const T*>(t.x) + b * t.xb + n * t.xn;
-  T* y = static_cast<T*>(t.y) + b * t.yb + n * t.yn;
-  // the first heads' values are on their way while the sines are formed
-  constexpr int U = NU == 1 ? 2 : 1;  // heads in flight
-  float va[U][NU][V], vb[U][NU][V];
-  auto fetch = [&](int h) {
+  const T* x = static_cast<const T*>(t.x) + b * t.xb + n * t.xn + h0 * t.xh;  // of the next head to fetch
+  T* y = static_cast<T*>(t.y) + b * t.yb + n * t.yn + h0 * t.yh;              // of the next head to store
+  constexpr int kAhead = NU > 1 ? 1 : sizeof(T) == 2 ? 4 : 2;  // heads in flight
+  Chunk<T, V> ra[kAhead][NU], rb[kAhead][NU];
+  auto fetch = [&](int h, int q) {
 #pragma unroll
-    for (int q = 0; q < U; ++q)
-#pragma unroll
-      for (int k = 0; k < NU; ++k)
-        if (on[k] && h + q < h1) {
-          load_chunk<T, V>(x + (h + q) * t.xh + ea[k], va[q][k]);
-          load_chunk<T, V>(x + (h + q) * t.xh + eb[k], vb[q][k]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < V; ++j) va[q][k][j] = vb[q][k][j] = 0.0f;
-        }
+    for (int k = 0; k < NU; ++k)
+      if (on[k] && h < h1) {
+        ra[q][k] = fetch_chunk<T, V>(x + ea[k]);
+        rb[q][k] = fetch_chunk<T, V>(x + eb[k]);
+      }
+    x += t.xh;
   };
-  fetch(h0);
+#pragma unroll
+  for (int q = 0; q < kAhead; ++q) fetch(h0 + q, q);
+  // the first heads' values are on their way while the sines are formed
+  // NORM: the weights go into the pairs' factors, u (w_u c) - v (w_v s) and v (w_v c) + u (w_u s);
+  // behind the rotated part, c and cv are the weights
+  float c[NU][V], s[NU][V], cv[NORM ? NU : 1][V], sv[NORM ? NU : 1][V];
 #pragma unroll
   for (int k = 0; k < NU; ++k) {
     const int u = lane + k * a.tpr;
-    if (on[k] && 2 * u * V < a.rot) {
-      angles<V>(a, b, n, u, c[k], s[k]);
-    } else {
+    const bool turns = on[k] && 2 * u * V < a.rot;
+    if (turns) angles<T, V>(a, b, n, u, c[k], s[k]);
+    if (NORM && on[k]) {
+      float wa[V], wb[V];
+      load_weight<V>(a, t.w, ea[k], eb[k], wa, wb);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        c[k][j] = 1.0f;
-        s[k][j] = 0.0f;
+        const float wu = first<V, HALF>(wa, wb, j), wv = second<V, HALF>(wa, wb, j);
+        const float cj = turns ? c[k][j] : 1.0f, sj = turns ? s[k][j] : 0.0f;
+        c[k][j] = wu * cj;
+        cv[k][j] = wv * cj;
+        s[k][j] = wv * sj;
+        sv[k][j] = wu * sj;
       }
     }
-    if (NORM && on[k]) load_weight<V>(a, t.w, ea[k], eb[k], wa[k], wb[k]);
   }
-  for (int h = h0; h < h1; h += U) {
-    if (h != h0) fetch(h);
+  for (int h = h0; h < h1; h += kAhead) {
 #pragma unroll
-    for (int q = 0; q < U; ++q) {
+    for (int q = 0; q < kAhead; ++q) {
+      if (h + q >= h1) break;  // uniform over the block
+      float va[NU][V], vb[NU][V];
+      float sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < NU; ++k)
+        if (on[k]) {
+          widen(ra[q][k], va[k]);
+          widen(rb[q][k], vb[k]);
+        }
+      fetch(h + q + kAhead, q);
+      float r = 1.0f;
       if (NORM) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int k = 0; k < NU; ++k)
-#pragma unroll
-          for (int j = 0; j < V; ++j) sum += va[q][k][j] * va[q][k][j] + vb[q][k][j] * vb[q][k][j];
-        sum = group_sum(sum, a.tpr);
-        const float r = 1.0f / sqrtf(sum * a.inv_d + a.eps);
 #pragma unroll
         for (int k = 0; k < NU; ++k)
           if (on[k]) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum += va[k][j] * va[k][j] + vb[k][j] * vb[k][j];
+          }
+        sum = group_sum(sum, a.tpr);
+        r = rsqrtf(sum * a.inv_d + a.eps);
+      }
+#pragma unroll
+      for (int k = 0; k < NU; ++k)
+        if (on[k]) {
+          const bool turns = 2 * (lane + k * a.tpr) * V < a.rot;
+          if (!NORM) {
+            if (turns) rotate<V, HALF>(va[k], vb[k], c[k], s[k]);
+          } else {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-              va[q][k][j] *= r * wa[k][j];
-              vb[q][k][j] *= r * wb[k][j];
+              float &u = first<V, HALF>(va[k], vb[k], j), &v = second<V, HALF>(va[k], vb[k], j);
+              float x = u * c[k][j], y = v * cv[k][j];
+              if (turns) {  // no 0 x inf where nothing turns
+                x -= v * s[k][j];
+                y += u * sv[k][j];
+              }
+              u = x * r;
+              v = y * r;
             }
           }
-      }
-      if (h + q < h1) {
-#pragma unroll
-        for (int k = 0; k < NU; ++k)
-          if (on[k]) {
-            if (2 * (lane + k * a.tpr) * V < a.rot) rotate<V, HALF>(va[q][k], vb[q][k], c[k], s[k]);
-            store_chunk<T, V>(y + (h + q) * t.yh + ea[k], va[q][k]);
-            store_chunk<T, V>(y + (h + q) * t.yh + eb[k], vb[q][k]);
-          }
-      }
+          store_chunk(y + ea[k], va[k]);
+          store_chunk(y + eb[k], vb[k]);
+        }
+      y += t.yh;
     }
   }
 }
@@ -244,12 +307,17 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
 // dy backwards, xh = x r, r = 1 / sqrt(mean(x^2) + eps):
 //   dw = sum over tokens and heads of g xh,
 //   dx = r (g w - xh mean(g w xh)).
-// Blocks walk over token tiles; each keeps its dw in registers and leaves one
-// row of partial sums, which norm_dw_kernel adds in a fixed order.
+// One round of blocks, shared between q and k by their heads, walks over token
+// tiles; each block keeps its dw in registers and leaves one row of partial sums,
+// which norm_dw_kernel adds in a fixed order.
 template <typename T, int V, int NU, bool HALF>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, NU == 1 ? 3 : 1) norm_rope_bwd_kernel(const RopeArgs a) {
   extern __shared__ float dw_sh[];  // [groups][d]
-  const RopeTensor& t = a.t[blockIdx.y];
+  asm volatile("griddepcontrol.launch_dependents;");  // the sum's launch runs behind this kernel
+  const int tensor = int(blockIdx.x) < a.split ? 0 : 1;
+  const unsigned block = tensor == 0 ? blockIdx.x : blockIdx.x - a.split;
+  const unsigned blocks = tensor == 0 ? a.split : gridDim.x - a.split;
+  const RopeTensor& t = a.t[tensor];
   const int lane = threadIdx.x % a.tpr, group = threadIdx.x / a.tpr, groups = kThreads / a.tpr;
   float wa[NU][V], wb[NU][V], da[NU][V], db[NU][V];
   int ea[NU], eb[NU];
@@ -264,56 +332,79 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const RopeArgs 
     for (int j = 0; j < V; ++j) da[k][j] = db[k][j] = 0.0f;
   }
   const unsigned total = unsigned(a.B) * unsigned(a.N), tiles = (total + groups - 1) / groups;
-  const int ranges = (t.H + a.hpg - 1) / a.hpg;
-  for (unsigned long long item = blockIdx.x; item < (unsigned long long)tiles * ranges; item += gridDim.x) {
-    const unsigned tile = unsigned(item / ranges), range = unsigned(item - (unsigned long long)tile * ranges);
+  constexpr int h0 = 0;
+  const int h1 = t.H;
+  for (unsigned tile = block; tile < tiles; tile += blocks) {
     const unsigned tok = tile * groups + group;
     const bool live = tok < total;
     const int b = live ? int(tok / unsigned(a.N)) : 0, n = live ? int(tok - unsigned(b) * unsigned(a.N)) : 0;
-    const int h0 = range * a.hpg, h1 = min(t.H, h0 + a.hpg);
+    const T* x = static_cast<const T*>(t.x) + b * t.xb + n * t.xn + h0 * t.xh;
+    const T* dy = static_cast<const T*>(t.dy) + b * t.gb + n * t.gn + h0 * t.gh;
+    T* dx = static_cast<T*>(t.y) + b * t.yb + n * t.yn + h0 * t.yh;
+    constexpr int kAhead = NU == 1 && sizeof(T) == 2 ? 2 : 1;  // heads in flight
+    Chunk<T, V> rx[kAhead][NU][2], rg[kAhead][NU][2];
+    auto fetch = [&](int h, int q) {
+#pragma unroll
+      for (int k = 0; k < NU; ++k)
+        if (live && has[k] && h < h1) {
+          rx[q][k][0] = fetch_chunk<T, V>(x + ea[k]);
+          rx[q][k][1] = fetch_chunk<T, V>(x + eb[k]);
+          rg[q][k][0] = fetch_chunk<T, V>(dy + ea[k]);
+          rg[q][k][1] = fetch_chunk<T, V>(dy + eb[k]);
+        }
+      x += t.xh;
+      dy += t.gh;
+    };
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) fetch(h0 + q, q);
     float c[NU][V], s[NU][V];
 #pragma unroll
     for (int k = 0; k < NU; ++k)
-      if (live && has[k] && 2 * (lane + k * a.tpr) * V < a.rot) angles<V>(a, b, n, lane + k * a.tpr, c[k], s[k]);
-    const T* x = static_cast<const T*>(t.x) + b * t.xb + n * t.xn;
-    const T* dy = static_cast<const T*>(t.dy) + b * t.gb + n * t.gn;
-    T* dx = static_cast<T*>(t.y) + b * t.yb + n * t.yn;
-    for (int h = h0; h < h1; ++h) {
-      float xa[NU][V], xb[NU][V], ga[NU][V], gb[NU][V];
-      float sxx = 0.0f, sgx = 0.0f;
+      if (live && has[k] && 2 * (lane + k * a.tpr) * V < a.rot) angles<T, V>(a, b, n, lane + k * a.tpr, c[k], s[k]);
+    for (int h = h0; h < h1; h += kAhead) {
 #pragma unroll
-      for (int k = 0; k < NU; ++k) {
-        if (live && has[k]) {
-          load_chunk<T, V>(x + h * t.xh + ea[k], xa[k]);
-          load_chunk<T, V>(x + h * t.xh + eb[k], xb[k]);
-          load_chunk<T, V>(dy + h * t.gh + ea[k], ga[k]);
-          load_chunk<T, V>(dy + h * t.gh + eb[k], gb[k]);
-          if (2 * (lane + k * a.tpr) * V < a.rot) rotate<V, HALF>(ga[k], gb[k], c[k], s[k]);
+      for (int q = 0; q < kAhead; ++q) {
+        if (h + q >= h1) break;  // uniform over the block
+        float xa[NU][V], xb[NU][V], ga[NU][V], gb[NU][V];
+        float sxx = 0.0f, sgx = 0.0f;
 #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            sxx += xa[k][j] * xa[k][j] + xb[k][j] * xb[k][j];
-            sgx += ga[k][j] * wa[k][j] * xa[k][j] + gb[k][j] * wb[k][j] * xb[k][j];
+        for (int k = 0; k < NU; ++k)
+          if (live && has[k]) {
+            widen(rx[q][k][0], xa[k]);
+            widen(rx[q][k][1], xb[k]);
+            widen(rg[q][k][0], ga[k]);
+            widen(rg[q][k][1], gb[k]);
           }
-        }
+        fetch(h + q + kAhead, q);
+#pragma unroll
+        for (int k = 0; k < NU; ++k)
+          if (live && has[k]) {
+            if (2 * (lane + k * a.tpr) * V < a.rot) rotate<V, HALF>(ga[k], gb[k], c[k], s[k]);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              sxx += xa[k][j] * xa[k][j] + xb[k][j] * xb[k][j];
+              sgx += wa[k][j] * (ga[k][j] * xa[k][j]) + wb[k][j] * (gb[k][j] * xb[k][j]);
+            }
+          }
+        group_sum2(sxx, sgx, a.tpr);
+        const float r = rsqrtf(sxx * a.inv_d + a.eps);
+        const float m = sgx * r * a.inv_d;  // mean(g w xh)
+#pragma unroll
+        for (int k = 0; k < NU; ++k)
+          if (live && has[k]) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              const float ha = xa[k][j] * r, hb = xb[k][j] * r;
+              da[k][j] += ga[k][j] * ha;
+              db[k][j] += gb[k][j] * hb;
+              xa[k][j] = r * (ga[k][j] * wa[k][j] - ha * m);
+              xb[k][j] = r * (gb[k][j] * wb[k][j] - hb * m);
+            }
+            store_chunk(dx + ea[k], xa[k]);
+            store_chunk(dx + eb[k], xb[k]);
+          }
+        dx += t.yh;
       }
-      sxx = group_sum(sxx, a.tpr);
-      sgx = group_sum(sgx, a.tpr);
-      const float r = 1.0f / sqrtf(sxx * a.inv_d + a.eps);
-      const float m = sgx * r * a.inv_d;  // mean(g w xh)
-#pragma unroll
-      for (int k = 0; k < NU; ++k)
-        if (live && has[k]) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const float ha = xa[k][j] * r, hb = xb[k][j] * r;
-            da[k][j] += ga[k][j] * ha;
-            db[k][j] += gb[k][j] * hb;
-            xa[k][j] = r * (ga[k][j] * wa[k][j] - ha * m);
-            xb[k][j] = r * (gb[k][j] * wb[k][j] - hb * m);
-          }
-          store_chunk<T, V>(dx + h * t.yh + ea[k], xa[k]);
-          store_chunk<T, V>(dx + h * t.yh + eb[k], xb[k]);
-        }
     }
   }
   if (t.dw == nullptr) return;  // uniform over the block
@@ -330,7 +421,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const RopeArgs 
   for (int i = threadIdx.x; i < a.d; i += kThreads) {
     float sum = 0.0f;
     for (int g = 0; g < groups; ++g) sum += dw_sh[g * a.d + i];
-    a.partial[(size_t(blockIdx.y) * gridDim.x + blockIdx.x) * a.d + i] = sum;
+    a.partial[size_t(blockIdx.x) * a.d + i] = sum;
   }
 }
 
@@ -338,12 +429,15 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const RopeArgs 
 // column, then the slices. One block per 32 columns of one tensor.
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const RopeArgs a, int rows) {
   __shared__ float part[32][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial rows are written
   void* dw = a.t[blockIdx.y].dw;
+  const int from = blockIdx.y == 0 ? 0 : a.split, to = blockIdx.y == 0 ? a.split : rows;
   if (dw == nullptr) return;
   const int col = blockIdx.x * 32 + threadIdx.x % 32, slice = threadIdx.x / 32;
   float sum = 0.0f;
   if (col < a.d)
-    for (int r = slice; r < rows; r += 32) sum += a.partial[(size_t(blockIdx.y) * rows + r) * a.d + col];
+#pragma unroll 8
+    for (int r = from + slice; r < to; r += 32) sum += a.partial[size_t(r) * a.d + col];
   part[slice][threadIdx.x % 32] = sum;
   __syncthreads();
   if (slice == 0 && col < a.d) {
@@ -381,37 +475,39 @@ cudaError_t launch_bwd(const RopeArgs& a, dim3 grid, cudaStream_t s) {
     norm_rope_bwd_kernel<T, V, NU, false><<<grid, kThreads, sh, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (a.t[0].dw == nullptr && a.t[1].dw == nullptr)) return e;
-  norm_dw_kernel<<<dim3((a.d + 31) / 32, grid.y), 1024, 0, s>>>(a, int(grid.x));
-  return cudaGetLastError();
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((a.d + 31) / 32, 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_dw_kernel, a, int(grid.x));
 }
 
-// Values per chunk: the widest of `widths` that the pair layout, the strides and the addresses allow.
+// Values per chunk: 4 where the pair layout, the strides and the addresses allow them, else 1.
 int chunk_width(const RopeArgs& a, int tensors, bool bwd) {
   const int size = a.dtype == SLA_FP32 ? 4 : 2;
-  for (int v : {8, 4}) {
-    if (v * size > 16) continue;
-    if (a.d % (2 * v) != 0 || a.rot % (2 * v) != 0) continue;
-    bool ok = true;
-    for (int i = 0; i < tensors; ++i) {
-      const RopeTensor& t = a.t[i];
-      auto fits = [&](const void* p, long long b, long long n, long long h) {
-        return reinterpret_cast<uintptr_t>(p) % (size_t(v) * size) == 0 && b % v == 0 && n % v == 0 && h % v == 0;
-      };
-      ok = ok && fits(t.x, t.xb, t.xn, t.xh) && fits(t.y, t.yb, t.yn, t.yh) &&
-           (!bwd || fits(t.dy, t.gb, t.gn, t.gh));
-    }
-    if (ok) return v;
+  constexpr int v = 4;
+  bool ok = a.d % (2 * v) == 0 && a.rot % (2 * v) == 0;
+  for (int i = 0; i < tensors; ++i) {
+    const RopeTensor& t = a.t[i];
+    auto fits = [&](const void* p, long long b, long long n, long long h) {
+      return reinterpret_cast<uintptr_t>(p) % (size_t(v) * size) == 0 && b % v == 0 && n % v == 0 && h % v == 0;
+    };
+    ok = ok && fits(t.x, t.xb, t.xn, t.xh) && fits(t.y, t.yb, t.yn, t.yh) && (!bwd || fits(t.dy, t.gb, t.gn, t.gh));
   }
-  return 1;
+  return ok ? v : 1;
 }
 
 }  // namespace
 
-// Blocks of the backward: what two waves of four blocks per SM hold; also the rows of partial sums.
-int rope_bwd_blocks(long long tokens, int heads) {
-  // tokens per block are at least 8 (32 lanes a row), head ranges of at least 1
-  const long long most = ((tokens + 7) / 8) * heads;
-  return int(std::max(1LL, std::min<long long>(most, kRopeBwdBlocks)));
+// Blocks of the backward over both tensors: one round of three per SM; also the rows of partial sums.
+int rope_bwd_blocks(long long tokens) {
+  const long long most = 2 * ((tokens + 7) / 8);  // a block takes at least 8 tokens (32 lanes a row)
+  return int(std::min<long long>(most, kRopeBwdBlocks));
 }
 
 cudaError_t launch_rope(RopeArgs a, int tensors, bool bwd, cudaStream_t s) {
@@ -428,15 +524,17 @@ cudaError_t launch_rope(RopeArgs a, int tensors, bool bwd, cudaStream_t s) {
   const long long want = (148 * 8 + tiles * tensors - 1) / (tiles * tensors);
   a.hpg = std::max<long long>(1, heads / std::min<long long>(want, heads));
   dim3 grid(unsigned(tiles), tensors, unsigned((heads + a.hpg - 1) / a.hpg));
-  if (bwd) grid = dim3(rope_bwd_blocks(tokens, heads), tensors, 1);
-#define SLA_ROPE(T)                                                       \
-  (v == 8   ? (bwd ? launch_bwd<T, 8, 1>(a, grid, s) : launch_fwd<T, 8, 1>(a, grid, s)) \
-   : v == 4 ? (bwd ? launch_bwd<T, 4, 1>(a, grid, s) : launch_fwd<T, 4, 1>(a, grid, s)) \
-            : (bwd ? launch_bwd<T, 1, 4>(a, grid, s) : launch_fwd<T, 1, 4>(a, grid, s)))
+  if (bwd) {
+    const int blocks = rope_bwd_blocks(tokens);
+    grid = dim3(blocks, 1, 1);
+    a.split = std::max(1, std::min(blocks - 1, int((long long)blocks * a.t[0].H / (a.t[0].H + a.t[1].H))));
+  }
+#define SLA_ROPE(T)                                                                  \
+  (v == 4 ? (bwd ? launch_bwd<T, 4, 1>(a, grid, s) : launch_fwd<T, 4, 1>(a, grid, s)) \
+          : (bwd ? launch_bwd<T, 1, 4>(a, grid, s) : launch_fwd<T, 1, 4>(a, grid, s)))
   if (a.dtype == SLA_BF16) return SLA_ROPE(__nv_bfloat16);
   if (a.dtype == SLA_FP16) return SLA_ROPE(__half);
-  if (v == 4) return bwd ? launch_bwd<float, 4, 1>(a, grid, s) : launch_fwd<float, 4, 1>(a, grid, s);
-  return bwd ? launch_bwd<float, 1, 4>(a, grid, s) : launch_fwd<float, 1, 4>(a, grid, s);
+  return SLA_ROPE(float);
 #undef SLA_ROPE
 }
 
