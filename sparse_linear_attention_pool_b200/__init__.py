@@ -436,6 +436,20 @@ def attention(q, k, v, *, N: Optional[int] = None, variant: str = "sla", k_crit:
     return _SLAFunction.apply(q, k, v, w_proj, alpha)
 
 
+def binding():
+    """The compiled PyTorch binding of the operators beside the attention. Raises if it is missing."""
+    import importlib
+
+    load()  # first: the binding links against it
+    try:
+        import torch  # noqa: F401  (its libraries, which the binding links against)
+
+        return importlib.import_module(f"{__name__}._sla_torch")
+    except ImportError as e:
+        raise RuntimeError(f"{_HERE}/_sla_torch.so not built or not loadable; run python -m "
+                           "sparse_linear_attention_pool_b200.build") from e
+
+
 # The operators beside the attention (modules rotary and prompt), loaded at their first use:
 # they import torch, which this module does not.
 _OPERATORS = {name: module for module, names in {

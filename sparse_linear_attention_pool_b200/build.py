@@ -1,4 +1,6 @@
-"""Builds the CUDA library libsla_b200.so in-tree for sm_100a with nvcc.
+"""Builds the CUDA library libsla_b200.so in-tree for sm_100a with nvcc, and the
+PyTorch binding of the operators beside the attention (_sla_torch.so) with the
+host compiler.
 
     python -m sparse_linear_attention_pool_b200.build [--force] [--verbose]
 """
@@ -15,6 +17,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 LIB = os.path.join(PKG, "libsla_b200.so")
+BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
+BINDING = os.path.join(PKG, "_sla_torch.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
          "--expt-relaxed-constexpr"]
@@ -27,22 +31,80 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def host_compiler() -> str:
+    """The g++ on PATH, as nvcc uses it ($CXX may name one that links its own copy of
+    libstdc++, which does not mix with torch's)."""
+    found = shutil.which("g++")
+    if not found:
+        raise RuntimeError("g++ not found")
+    return found
+
+
 def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
+def _stale(target: str, deps: list[str]) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    t = os.path.getmtime(target)
     return any(os.path.getmtime(p) > t for p in deps)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every .cu under csrc/ into one shared library; returns its path."""
-    if not force and not _stale():
-        return LIB
+    """Compile every .cu under csrc/ into one shared library, and the PyTorch binding;
+    returns the library's path."""
+    headers = glob.glob(os.path.join(INCLUDE, "*.h"))
+    with ThreadPoolExecutor(max_workers=1) as pool:
+        binding = None
+        if force or _stale(BINDING, [BINDING_SRC, *headers]):
+            binding = pool.submit(_build_binding)  # beside nvcc: half a minute of torch's headers
+        if force or _stale(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + headers):
+            _build_library(verbose)
+        if binding is not None:
+            obj = binding.result()
+            _link_binding(obj)
+    return LIB
+
+
+def _build_binding() -> str:
+    """Compiles torch_binding.cpp; returns the object's path."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    objdir = os.path.join(PKG, "_build")
+    os.makedirs(objdir, exist_ok=True)
+    obj = os.path.join(objdir, "torch_binding.o")
+    includes = [p for d in (*cpp_extension.include_paths(), os.path.join(_cuda_home(), "include"),
+                            sysconfig.get_paths()["include"]) for p in ("-isystem", d)]
+    cmd = [host_compiler(), "-O2", "-std=c++17", "-fPIC", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *includes, "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling {BINDING_SRC} failed:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    cmd = [host_compiler(), "-shared", "-o", tmp, obj, LIB, f"-L{libs}", "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
+def _cuda_home() -> str:
+    return os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+
+
+def _build_library(verbose: bool) -> None:
     objdir = os.path.join(PKG, "_build")
     os.makedirs(objdir, exist_ok=True)
 
@@ -59,12 +121,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
         objs = list(pool.map(compile_one, sources()))
     tmp = LIB + ".tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs]
+    cmd = [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-Xlinker", "-soname=libsla_b200.so", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

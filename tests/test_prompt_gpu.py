@@ -182,7 +182,7 @@ def test_streams_graphs_and_two_calls_of_one_plan(cuda_lib):
     q, k, v, _, _, _ = make(case, seed=6)
     q, k, v = q.cuda(), k.cuda(), v.cuda()
     plan = plan_of(sla, case)
-    assert plan._workspace > 0
+    assert plan.workspace_size > 0
     want, want_lse = sla.prompt_forward(q, k, v, plan)
     q2 = q.flip(1).contiguous()
     want2, _ = sla.prompt_forward(q2, k, v, plan)
@@ -293,7 +293,7 @@ def test_backward_with_split_query_tiles(cuda_lib):
     for case in (([2500], None, 4, 1, 64, True), ([3000], [140], 2, 1, 128, False)):
         q, k, v, do, lq, lk = make(case, seed=8)
         plan = plan_of(sla, case, grad=True)
-        assert plan._backward_workspace > 256 + plan.Tq * plan.Hq * 8  # split sums have a place of their own
+        assert plan.backward_workspace_size > 256 + plan.Tq * plan.Hq * 8  # split sums have a place of their own
         ref = R.prompt(q, k, v, lq, lk, case[5], do=do)
         o, lse = sla.prompt_forward(q.cuda(), k.cuda(), v.cuda(), plan)
         check_grads(case, sla.prompt_backward(q.cuda(), k.cuda(), v.cuda(), o, lse, do.cuda(), plan), ref, q, k)
