@@ -443,20 +443,23 @@ sla_status sla_prompt_plan(const sla_prompt_params* p, void* plan, size_t plan_b
  * where few rows read long caches, whose keys are then split among blocks). */
 size_t sla_prompt_workspace_size(const void* plan);
 
-/* O and, where lse is not NULL, lse [Tq, Hq] float32 = log sum exp(scale q.k)
- * over the keys that each query sees (what the backward reads). */
+/* O and, for the backward, where they are not NULL:
+ *   lse   [Tq, Hq] float32 = log sum exp(scale q.k) over the keys that each query sees;
+ *   rest  [Tq, Hq, d] bf16, 16-byte aligned = what O's rounding left off: with it the
+ *         gradients' row sums dO.O are those of the float32 O. */
 sla_status sla_prompt_forward(const sla_rows* q, const sla_rows* k, const sla_rows* v, const sla_rows* o, float* lse,
-                              const void* plan, size_t plan_bytes, void* plan_device, void* workspace,
+                              void* rest, const void* plan, size_t plan_bytes, void* plan_device, void* workspace,
                               size_t workspace_bytes, void* stream);
 
 /* Gradients of <dO, O> for a forward of the same plan, which must have been made
  * with backward = 1 (SLA_ERR_UNSUPPORTED otherwise).
  *   q, k, v, o, lse  the forward's inputs and results.
+ *   rest             the forward's, or NULL: dO.O from the rounded O alone.
  *   dq, dk, dv       outputs; a key head's dk, dv add up its group's query heads.
  * Deterministic. Rows behind the last sequence are neither read nor written. */
 size_t sla_prompt_backward_workspace_size(const void* plan);
 sla_status sla_prompt_backward(const sla_rows* q, const sla_rows* k, const sla_rows* v, const sla_rows* o,
-                               const float* lse, const sla_rows* dO, const sla_rows* dq, const sla_rows* dk,
+                               const float* lse, const void* rest, const sla_rows* dO, const sla_rows* dq, const sla_rows* dk,
                                const sla_rows* dv, const void* plan, size_t plan_bytes, void* plan_device,
                                void* workspace, size_t workspace_bytes, void* stream);
 

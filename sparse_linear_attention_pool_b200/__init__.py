@@ -140,9 +140,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sla_prompt_plan_size": (sz, [PP]),
         "sla_prompt_plan": (i, [PP, vp, sz]),
         "sla_prompt_workspace_size": (sz, [vp]),
-        "sla_prompt_forward": (i, [TP, TP, TP, TP, vp, vp, sz, vp, vp, sz, vp]),
+        "sla_prompt_forward": (i, [TP, TP, TP, TP, vp, vp, vp, sz, vp, vp, sz, vp]),
         "sla_prompt_backward_workspace_size": (sz, [vp]),
-        "sla_prompt_backward": (i, [TP, TP, TP, TP, vp, TP, TP, TP, TP, vp, sz, vp, vp, sz, vp]),
+        "sla_prompt_backward": (i, [TP, TP, TP, TP, vp, vp, TP, TP, TP, TP, vp, sz, vp, vp, sz, vp]),
         "sla_stage_timing": (i, [i]),
         "sla_stage_times": (i, [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int)]),
     }

@@ -65,6 +65,7 @@ struct PromptArgs {
   unsigned char* plan_dev;
   PromptTensor q, k, v, o;
   float* lse;                 // [Tq, Hq] or null
+  void* rest;                 // [Tq, Hq, d] bf16 or null
   float* part;                // [slots][tiles 128][d] partial O
   float* part_lse;            // [slots][tiles 128], log2
 };
@@ -73,6 +74,7 @@ struct PromptGradArgs {
   unsigned char* plan_dev;
   PromptTensor q, k, v, o, dO, dq, dk, dv;
   const float* lse;   // [Tq, Hq]
+  const void* rest;   // [Tq, Hq, d] bf16 or null
   float2* ld;         // [Hkv][Tq G]: (lse log2 e, rowsum dO O)
   float* part;        // [key slots][2][128][d] partial dK, dV
 };

@@ -389,7 +389,7 @@ size_t sla_prompt_workspace_size(const void* plan) {
 }
 
 sla_status sla_prompt_forward(const sla_rows* q, const sla_rows* k, const sla_rows* v, const sla_rows* o, float* lse,
-                              const void* plan, size_t plan_bytes, void* plan_device, void* workspace,
+                              void* rest, const void* plan, size_t plan_bytes, void* plan_device, void* workspace,
                               size_t workspace_bytes, void* stream) {
   const PromptPlan* p = plan_of(plan, plan_bytes);
   if (p == nullptr || plan_device == nullptr) return SLA_ERR_INVALID_ARG;
@@ -399,12 +399,13 @@ sla_status sla_prompt_forward(const sla_rows* q, const sla_rows* k, const sla_ro
   if (st == SLA_OK && p->Tk > 0) st = check_rows(k, p->Tk, p->Hkv, p->d, false, &a.k);
   if (st == SLA_OK && p->Tk > 0) st = check_rows(v, p->Tk, p->Hkv, p->d, false, &a.v);
   if (st != SLA_OK) return st;
-  if (!aligned(plan_device, 256) || !aligned(lse, 4)) return SLA_ERR_ALIGNMENT;
+  if (!aligned(plan_device, 256) || !aligned(lse, 4) || !aligned(rest, 16)) return SLA_ERR_ALIGNMENT;
   st = check_workspace(workspace, workspace_bytes, forward_workspace(*p));
   if (st != SLA_OK) return st;
   a.plan = p;
   a.plan_dev = static_cast<unsigned char*>(plan_device);
   a.lse = lse;
+  a.rest = rest;
   a.part = static_cast<float*>(workspace);
   a.part_lse = a.part + size_t(p->n_slots) * p->tiles * 128 * p->d;
   return launch_prompt_forward(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SLA_OK : SLA_ERR_CUDA;
@@ -416,7 +417,7 @@ size_t sla_prompt_backward_workspace_size(const void* plan) {
 }
 
 sla_status sla_prompt_backward(const sla_rows* q, const sla_rows* k, const sla_rows* v, const sla_rows* o,
-                               const float* lse, const sla_rows* dO, const sla_rows* dq, const sla_rows* dk,
+                               const float* lse, const void* rest, const sla_rows* dO, const sla_rows* dq, const sla_rows* dk,
                                const sla_rows* dv, const void* plan, size_t plan_bytes, void* plan_device,
                                void* workspace, size_t workspace_bytes, void* stream) {
   const PromptPlan* p = plan_of(plan, plan_bytes);
@@ -434,12 +435,13 @@ sla_status sla_prompt_backward(const sla_rows* q, const sla_rows* k, const sla_r
     if (st == SLA_OK) st = check_rows(dv, p->Tk, p->Hkv, p->d, true, &a.dv);
   }
   if (st != SLA_OK) return st;
-  if (!aligned(plan_device, 256) || !aligned(lse, 4)) return SLA_ERR_ALIGNMENT;
+  if (!aligned(plan_device, 256) || !aligned(lse, 4) || !aligned(rest, 16)) return SLA_ERR_ALIGNMENT;
   st = check_workspace(workspace, workspace_bytes, backward_workspace(*p));
   if (st != SLA_OK) return st;
   a.plan = p;
   a.plan_dev = static_cast<unsigned char*>(plan_device);
   a.lse = lse;
+  a.rest = rest;
   a.ld = static_cast<float2*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
                                     align256(size_t(p->Tq) * p->Hq * sizeof(float2)));

@@ -29,6 +29,7 @@ struct PromptGradDev {
   const PromptKeysJoin* kjoins;
   PromptTensor o, g, dq, dk, dv;
   const float* lse;
+  const __nv_bfloat16* rest;
   float2* ld;
   float* part;
   int Hq, Hkv, G, tpt, causal, row_tiles;
@@ -58,9 +59,12 @@ __global__ void __launch_bounds__(256) prompt_rowsum_kernel(const PromptGradDev 
                                                     h * a.o.head + lane * 8);
     const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.g.base) + t * a.g.row +
                                                     h * a.g.head + lane * 8);
-    const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+    uint4 z = make_uint4(0, 0, 0, 0);  // O = x + z
+    if (a.rest) z = *reinterpret_cast<const uint4*>(a.rest + row * D + lane * 8);
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w}, w[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sum += bf16_lo(u[i]) * bf16_lo(v[i]) + bf16_hi(u[i]) * bf16_hi(v[i]);
+    for (int i = 0; i < 4; ++i)
+      sum += (bf16_lo(u[i]) + bf16_lo(w[i])) * bf16_lo(v[i]) + (bf16_hi(u[i]) + bf16_hi(w[i])) * bf16_hi(v[i]);
   }
   for (int s = kLanes / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
   if (live && lane == 0) {
@@ -738,6 +742,7 @@ cudaError_t launch_prompt_backward(const PromptGradArgs& a, cudaStream_t s) {
   v.dk = a.dk;
   v.dv = a.dv;
   v.lse = a.lse;
+  v.rest = static_cast<const __nv_bfloat16*>(a.rest);
   v.ld = a.ld;
   v.part = a.part;
   v.Hq = p.Hq;

@@ -34,6 +34,7 @@ struct PromptDev {
   const PromptJoin* joins;
   __nv_bfloat16* o;
   long long o_row, o_head;
+  __nv_bfloat16* rest;
   float *lse, *part, *part_lse;
   int Hq, G, tpt, causal, tiles;
   long long Tq, Tk;
@@ -374,6 +375,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, FwdCfg<D, TILES>::
     const int head = it.head * a.G + g;
     const size_t prow = size_t(max(it.slot, 0)) * (a.tiles * 128) + (t * 128 + r);
     __nv_bfloat16* orow = a.o + token * a.o_row + head * a.o_head;
+    __nv_bfloat16* rest = a.rest ? a.rest + (token * a.Hq + head) * D : nullptr;
     float* part = a.part + prow * D;
 #pragma unroll 1
     for (int j = 0; j < D; j += 32) {
@@ -387,10 +389,15 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, FwdCfg<D, TILES>::
       if (!live) continue;
       if (it.slot < 0) {
 #pragma unroll
-        for (int x = 0; x < 32; x += 8)
-          *reinterpret_cast<uint4*>(orow + j + x) =
-              make_uint4(pack_bf16(o[x], o[x + 1]), pack_bf16(o[x + 2], o[x + 3]), pack_bf16(o[x + 4], o[x + 5]),
-                         pack_bf16(o[x + 6], o[x + 7]));
+        for (int x = 0; x < 32; x += 8) {
+          const uint4 w = make_uint4(pack_bf16(o[x], o[x + 1]), pack_bf16(o[x + 2], o[x + 3]),
+                                     pack_bf16(o[x + 4], o[x + 5]), pack_bf16(o[x + 6], o[x + 7]));
+          *reinterpret_cast<uint4*>(orow + j + x) = w;
+          if (rest)
+            *reinterpret_cast<uint4*>(rest + j + x) =
+                make_uint4(pack_rest(o[x], o[x + 1], w.x), pack_rest(o[x + 2], o[x + 3], w.y),
+                           pack_rest(o[x + 4], o[x + 5], w.z), pack_rest(o[x + 6], o[x + 7], w.w));
+        }
       } else {
 #pragma unroll
         for (int x = 0; x < 32; x += 4)
@@ -458,7 +465,13 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const PromptDev a) {
   const int head = jn.head * a.G + g;
   __nv_bfloat16* orow = a.o + token * a.o_row + head * a.o_head + lane * V;
 #pragma unroll
-  for (int x = 0; x < V; x += 2) *reinterpret_cast<uint32_t*>(orow + x) = pack_bf16(o[x] * inv, o[x + 1] * inv);
+  for (int x = 0; x < V; x += 2) {
+    const uint32_t w = pack_bf16(o[x] * inv, o[x + 1] * inv);
+    *reinterpret_cast<uint32_t*>(orow + x) = w;
+    if (a.rest)
+      *reinterpret_cast<uint32_t*>(a.rest + (token * a.Hq + head) * D + lane * V + x) =
+          pack_rest(o[x] * inv, o[x + 1] * inv, w);
+  }
   if (lane == 0 && a.lse)
     a.lse[token * a.Hq + head] = den == 0.0f ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
 }
@@ -506,6 +519,7 @@ cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s) {
   v.o = static_cast<__nv_bfloat16*>(a.o.base);
   v.o_row = a.o.row;
   v.o_head = a.o.head;
+  v.rest = static_cast<__nv_bfloat16*>(a.rest);
   v.lse = a.lse;
   v.part = a.part;
   v.part_lse = a.part_lse;

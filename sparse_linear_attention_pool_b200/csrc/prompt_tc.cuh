@@ -43,6 +43,10 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// What rounding (a, b) to the bf16 pair w left off, as a bf16 pair
+__device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t w) {
+  return pack_bf16(a - bf16_lo(w), b - bf16_hi(w));
+}
 // Registers per thread of this warpgroup, from here on (all four warps run it)
 template <int n>
 __device__ __forceinline__ void reg_inc() {

@@ -389,30 +389,32 @@ sla_rows out_rows(Tensor& out, const Tensor& x, int64_t T, int64_t H, const Prom
   return {out.data_ptr(), out.stride(0), out.stride(1)};
 }
 
-std::tuple<Tensor, Tensor> run_forward(Tensor q, Tensor k, Tensor v, const PromptPlan& p, Tensor out, bool want_lse,
-                                       const OptTensor& workspace) {
+std::tuple<Tensor, Tensor, Tensor> run_forward(Tensor q, Tensor k, Tensor v, const PromptPlan& p, Tensor out,
+                                               bool want_lse, bool want_rest, const OptTensor& workspace) {
   const sla_rows rq = rows_of(q, p.Tq, p.Hq, p, "q"), rk = rows_of(k, p.Tk, p.Hkv, p, "k"),
                  rv = rows_of(v, p.Tk, p.Hkv, p, "v");
   const sla_rows ro = out_rows(out, q, p.Tq, p.Hq, p, "out");
-  Tensor lse, ws;
+  Tensor lse, rest, ws;
+  if (want_rest) rest = at::empty({p.Tq, p.Hq, p.d}, q.options());
   if (want_lse) lse = at::empty({p.Tq, p.Hq}, q.options().dtype(at::kFloat));
   if (workspace)
     ws = *workspace;
   else if (p.forward_workspace > 0)
     ws = at::empty({p.forward_workspace}, q.options().dtype(at::kByte));
-  check_status(sla_prompt_forward(&rq, &rk, &rv, &ro, want_lse ? lse.data_ptr<float>() : nullptr, p.host.data(),
-                                  p.bytes, p.device.data_ptr(), ws.defined() ? ws.data_ptr() : nullptr,
+  check_status(sla_prompt_forward(&rq, &rk, &rv, &ro, want_lse ? lse.data_ptr<float>() : nullptr,
+                                  want_rest ? rest.data_ptr() : nullptr, p.host.data(), p.bytes,
+                                  p.device.data_ptr(), ws.defined() ? ws.data_ptr() : nullptr,
                                   ws.defined() ? ws.nbytes() : 0, stream_of(q)),
                "sla_prompt_forward");
-  return {out, lse};
+  return {out, lse, rest};
 }
 
 void check_grad(const PromptPlan& p) {
   TORCH_CHECK_VALUE(p.grad, "the plan was made without the backward pass (grad=True)");
 }
 
-std::tuple<Tensor, Tensor, Tensor> run_backward(Tensor q, Tensor k, Tensor v, Tensor o, const Tensor& lse, Tensor dO,
-                                                const PromptPlan& p, Tensor dq, Tensor dk, Tensor dv,
+std::tuple<Tensor, Tensor, Tensor> run_backward(Tensor q, Tensor k, Tensor v, Tensor o, const Tensor& lse,
+                                                const Tensor& rest, Tensor dO, const PromptPlan& p, Tensor dq, Tensor dk, Tensor dv,
                                                 const OptTensor& workspace) {
   const sla_rows rq = rows_of(q, p.Tq, p.Hq, p, "q"), rk = rows_of(k, p.Tk, p.Hkv, p, "k"),
                  rv = rows_of(v, p.Tk, p.Hkv, p, "v"), ro = rows_of(o, p.Tq, p.Hq, p, "o"),
@@ -420,11 +422,17 @@ std::tuple<Tensor, Tensor, Tensor> run_backward(Tensor q, Tensor k, Tensor v, Te
   TORCH_CHECK_VALUE(lse.scalar_type() == at::kFloat && lse.dim() == 2 && lse.size(0) == p.Tq && lse.size(1) == p.Hq &&
                         lse.is_contiguous() && lse.device() == p.device.device(),
                     "lse: prompt_forward's [", p.Tq, ", ", p.Hq, "] float32");
+  if (rest.defined())
+    TORCH_CHECK_VALUE(rest.scalar_type() == at::kBFloat16 && rest.is_contiguous() && rest.dim() == 3 &&
+                          rest.size(0) == p.Tq && rest.size(1) == p.Hq && rest.size(2) == p.d &&
+                          rest.device() == p.device.device(),
+                      "rest: prompt_forward's [", p.Tq, ", ", p.Hq, ", ", p.d, "] bfloat16");
   const bool fresh = !dq.defined();
   const sla_rows oq = out_rows(dq, q, p.Tq, p.Hq, p, "dq"), ok = out_rows(dk, k, p.Tk, p.Hkv, p, "dk"),
                  ov = out_rows(dv, v, p.Tk, p.Hkv, p, "dv");
   const Tensor ws = workspace ? *workspace : at::empty({p.backward_workspace}, q.options().dtype(at::kByte));
-  check_status(sla_prompt_backward(&rq, &rk, &rv, &ro, lse.data_ptr<float>(), &rg, &oq, &ok, &ov, p.host.data(),
+  check_status(sla_prompt_backward(&rq, &rk, &rv, &ro, lse.data_ptr<float>(),
+                                   rest.defined() ? rest.data_ptr() : nullptr, &rg, &oq, &ok, &ov, p.host.data(),
                                    p.bytes, p.device.data_ptr(), ws.data_ptr(), ws.nbytes(), stream_of(q)),
                "sla_prompt_backward");
   if (fresh) {
@@ -443,31 +451,33 @@ struct PlanMeta : torch::CustomClassHolder {
 struct PromptFunction : torch::autograd::Function<PromptFunction> {
   static Tensor forward(AutogradContext* ctx, const Tensor& q, const Tensor& k, const Tensor& v,
                         c10::intrusive_ptr<PlanMeta> meta) {
-    auto [o, lse] = run_forward(q, k, v, *meta->plan, Tensor(), true, {});
+    auto [o, lse, rest] = run_forward(q, k, v, *meta->plan, Tensor(), true, true, {});
     ctx->saved_data["plan"] = c10::IValue::make_capsule(meta);
-    ctx->save_for_backward({q, k, v, o, lse});
+    ctx->save_for_backward({q, k, v, o, lse, rest});
     return o;
   }
   static variable_list backward(AutogradContext* ctx, variable_list grads) {
     TORCH_CHECK(!at::GradMode::is_enabled(), "prompt_attention is not differentiable twice");
     const auto meta = c10::static_intrusive_pointer_cast<PlanMeta>(ctx->saved_data["plan"].toCapsule());
     const auto s = ctx->get_saved_variables();
-    auto [dq, dk, dv] = run_backward(s[0], s[1], s[2], s[3], s[4], grads[0], *meta->plan, Tensor(), Tensor(),
+    auto [dq, dk, dv] = run_backward(s[0], s[1], s[2], s[3], s[4], s[5], grads[0], *meta->plan, Tensor(), Tensor(),
                                      Tensor(), {});
     return {dq, dk, dv, Tensor()};
   }
 };
 
-std::tuple<Tensor, OptTensor> prompt_forward(const Tensor& q, const Tensor& k, const Tensor& v, const PlanPtr& plan,
-                                             const OptTensor& out, bool want_lse, const OptTensor& workspace) {
+std::tuple<Tensor, OptTensor, OptTensor> prompt_forward(const Tensor& q, const Tensor& k, const Tensor& v,
+                                                        const PlanPtr& plan, const OptTensor& out, bool want_lse,
+                                                        bool want_rest, const OptTensor& workspace) {
   at::NoGradGuard no_grad;
   c10::OptionalDeviceGuard guard(plan->device.device());
-  auto [o, lse] = run_forward(q, k, v, *plan, out ? *out : Tensor(), want_lse, workspace);
-  return {o, want_lse ? OptTensor(lse) : OptTensor()};
+  auto [o, lse, rest] = run_forward(q, k, v, *plan, out ? *out : Tensor(), want_lse, want_rest, workspace);
+  return {o, want_lse ? OptTensor(lse) : OptTensor(), want_rest ? OptTensor(rest) : OptTensor()};
 }
 
 std::tuple<Tensor, Tensor, Tensor> prompt_backward(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& o,
-                                                   const Tensor& lse, const Tensor& dO, const PlanPtr& plan,
+                                                   const Tensor& lse, const OptTensor& rest, const Tensor& dO,
+                                                   const PlanPtr& plan,
                                                    const std::optional<std::tuple<Tensor, Tensor, Tensor>>& out,
                                                    const OptTensor& workspace) {
   at::NoGradGuard no_grad;
@@ -475,7 +485,7 @@ std::tuple<Tensor, Tensor, Tensor> prompt_backward(const Tensor& q, const Tensor
   c10::OptionalDeviceGuard guard(plan->device.device());
   Tensor dq, dk, dv;
   if (out) std::tie(dq, dk, dv) = *out;
-  return run_backward(q, k, v, o, lse, dO, *plan, dq, dk, dv, workspace);
+  return run_backward(q, k, v, o, lse, rest ? *rest : Tensor(), dO, *plan, dq, dk, dv, workspace);
 }
 
 Tensor prompt_attention(const Tensor& q, const Tensor& k, const Tensor& v, const PlanPtr& plan) {
@@ -484,7 +494,7 @@ Tensor prompt_attention(const Tensor& q, const Tensor& k, const Tensor& v, const
     check_grad(*plan);
     return PromptFunction::apply(q, k, v, c10::make_intrusive<PlanMeta>(plan));
   }
-  return std::get<0>(run_forward(q, k, v, *plan, Tensor(), false, {}));
+  return std::get<0>(run_forward(q, k, v, *plan, Tensor(), false, false, {}));
 }
 
 }  // namespace

@@ -78,23 +78,29 @@ def prompt_plan(lens_q: Sequence[int], lens_k: Optional[Sequence[int]] = None, *
                       int(Hq), int(Hkv), int(d), bool(causal), grad)
 
 
-def prompt_forward(q, k, v, plan: PromptPlan, *, out=None, want_lse: bool = True, workspace=None, stream=None):
-    """(O, lse): sla_prompt_forward. O [rows of q, Hq, d]; lse [Tq, Hq] float32 or None.
-    Rows of O behind the plan's last token are not written."""
+def prompt_forward(q, k, v, plan: PromptPlan, *, out=None, want_lse: bool = True, want_rest: bool = False,
+                   workspace=None, stream=None):
+    """(O, lse), or (O, lse, rest) with want_rest: sla_prompt_forward. O [rows of q, Hq, d]; lse
+    [Tq, Hq] float32 or None; rest [Tq, Hq, d], what O's rounding left off, which makes the
+    backward's gradients a little more exact. Rows of O behind the plan's last token are not written."""
+    args = (q, k, v, plan._c, out, want_lse, want_rest, workspace)
     if stream is not None:
         with on_stream(stream, q.device):
-            return _sla.prompt_forward(q, k, v, plan._c, out, want_lse, workspace)
-    return _sla.prompt_forward(q, k, v, plan._c, out, want_lse, workspace)
+            made = _sla.prompt_forward(*args)
+    else:
+        made = _sla.prompt_forward(*args)
+    return made if want_rest else made[:2]
 
 
-def prompt_backward(q, k, v, o, lse, do, plan: PromptPlan, *, out=None, workspace=None, stream=None):
-    """(dq, dk, dv): sla_prompt_backward for the upstream do of a prompt_forward's o and lse.
-    out: a triple of tensors to write to. Gradient rows behind the plan's last token are
-    zero, or with `out` as they were."""
+def prompt_backward(q, k, v, o, lse, do, plan: PromptPlan, *, rest=None, out=None, workspace=None, stream=None):
+    """(dq, dk, dv): sla_prompt_backward for the upstream do of a prompt_forward's o, lse and
+    (optionally) rest. out: a triple of tensors to write to. Gradient rows behind the plan's
+    last token are zero, or with `out` as they were."""
+    args = (q, k, v, o, lse, rest, do, plan._c, out, workspace)
     if stream is not None:
         with on_stream(stream, q.device):
-            return _sla.prompt_backward(q, k, v, o, lse, do, plan._c, out, workspace)
-    return _sla.prompt_backward(q, k, v, o, lse, do, plan._c, out, workspace)
+            return _sla.prompt_backward(*args)
+    return _sla.prompt_backward(*args)
 
 
 def prompt_attention(q, k, v, plan: PromptPlan, *, stream=None):

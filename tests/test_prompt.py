@@ -193,14 +193,14 @@ CALLS = [
 
 @pytest.mark.parametrize("kw,code", CALLS + [
     (dict(o=None), "INVALID_ARG"), (dict(o=rows(row=64)), "INVALID_ARG"), (dict(o=rows(head=32)), "INVALID_ARG"),
-    (dict(lse=0x2002), "ALIGNMENT"),
+    (dict(lse=0x2002), "ALIGNMENT"), (dict(rest=0x2008), "ALIGNMENT"),
 ])
 def test_forward_refuses_on_the_host(lib, kw, code):
     """Fake device addresses: every call is refused before anything is enqueued."""
     plan = sla.prompt_plan([5, 90], Hq=4, Hkv=2, d=64, device="cpu")
-    a = dict(q=rows(), k=rows(), v=rows(), o=rows(), lse=None, plan=plan.host, size=len(plan.host.raw), dev=0x100000)
+    a = dict(q=rows(), k=rows(), v=rows(), o=rows(), lse=None, rest=None, plan=plan.host, size=len(plan.host.raw), dev=0x100000)
     a.update(kw)
-    st = lib.sla_prompt_forward(a["q"], a["k"], a["v"], a["o"], a["lse"], a["plan"], a["size"], a["dev"], None, 0, None)
+    st = lib.sla_prompt_forward(a["q"], a["k"], a["v"], a["o"], a["lse"], a["rest"], a["plan"], a["size"], a["dev"], None, 0, None)
     assert st == getattr(sla, "SLA_ERR_" + code)
 
 
@@ -210,22 +210,22 @@ def test_forward_refuses_a_missing_workspace(lib):
     assert need > 0
     r = rows()
     for ws, n in ((None, 1 << 30), (0x200080, 1 << 30), (0x200000, need - 1)):
-        assert lib.sla_prompt_forward(r, r, r, r, None, plan.host, len(plan.host.raw), 0x100000, ws, n,
+        assert lib.sla_prompt_forward(r, r, r, r, None, None, plan.host, len(plan.host.raw), 0x100000, ws, n,
                                       None) == sla.SLA_ERR_WORKSPACE
 
 
 @pytest.mark.parametrize("kw,code", CALLS + [
     (dict(o=None), "INVALID_ARG"), (dict(do=rows(base=0x10004)), "ALIGNMENT"), (dict(lse=None), "INVALID_ARG"),
     (dict(dq=rows(head=32)), "INVALID_ARG"), (dict(dk=None), "INVALID_ARG"), (dict(dv=rows(row=64)), "INVALID_ARG"),
-    (dict(ws=None), "WORKSPACE"), (dict(ws=0x200010), "WORKSPACE"), (dict(n=64), "WORKSPACE"),
+    (dict(rest=0x2008), "ALIGNMENT"), (dict(ws=None), "WORKSPACE"), (dict(ws=0x200010), "WORKSPACE"), (dict(n=64), "WORKSPACE"),
     (dict(serve=True), "UNSUPPORTED"),
 ])
 def test_backward_refuses_on_the_host(lib, kw, code):
     plan = sla.prompt_plan([5, 90], Hq=4, Hkv=2, d=64, grad=not kw.pop("serve", False), device="cpu")
-    a = dict(q=rows(), k=rows(), v=rows(), o=rows(), lse=0x3000, do=rows(), dq=rows(), dk=rows(), dv=rows(),
+    a = dict(q=rows(), k=rows(), v=rows(), o=rows(), lse=0x3000, rest=None, do=rows(), dq=rows(), dk=rows(), dv=rows(),
              plan=plan.host, size=len(plan.host.raw), dev=0x100000, ws=0x200000, n=1 << 30)
     a.update(kw)
-    st = lib.sla_prompt_backward(a["q"], a["k"], a["v"], a["o"], a["lse"], a["do"], a["dq"], a["dk"], a["dv"],
+    st = lib.sla_prompt_backward(a["q"], a["k"], a["v"], a["o"], a["lse"], a["rest"], a["do"], a["dq"], a["dk"], a["dv"],
                                  a["plan"], a["size"], a["dev"], a["ws"], a["n"], None)
     assert st == getattr(sla, "SLA_ERR_" + code)
 

@@ -282,9 +282,15 @@ def test_backward(cuda_lib, case):
     check_forward(case, o.detach(), None, ref, q, k)
     check_grads(case, grads, ref, q, k)
     # bit for bit, again
-    o, lse = sla.prompt_forward(*(t.detach() for t in leaves), plan)
-    again = sla.prompt_backward(*(t.detach() for t in leaves), o, lse, do.cuda(), plan)
+    o, lse, rest = sla.prompt_forward(*(t.detach() for t in leaves), plan, want_rest=True)
+    again = sla.prompt_backward(*(t.detach() for t in leaves), o, lse, do.cuda(), plan, rest=rest)
     assert all(torch.equal(a, b) for a, b in zip(grads, again))
+    # O + rest is the float32 O: two bf16 hold 16 bits of it
+    e = score_error(case[4], q, k, 1 / math.sqrt(case[4]))
+    err = (o.cpu().double() + rest.cpu().double() - ref["o"]).abs()
+    assert (err <= (H8 + 3 * e) * ref["o_size"] * 1.01 + 2.0 ** -15 * ref["o"].abs() + 1e-30).all()
+    # without the rest the gradients hold the same bounds
+    check_grads(case, sla.prompt_backward(*(t.detach() for t in leaves), o, lse, do.cuda(), plan), ref, q, k)
 
 
 def test_backward_with_split_query_tiles(cuda_lib):
@@ -370,8 +376,8 @@ def test_backward_graph_and_shared_leaves(cuda_lib):
     # k and v the same tensor, and broadcast heads: gradients add up
     kv = k.clone().requires_grad_(True)
     (dkv,) = torch.autograd.grad(sla.prompt_attention(q, kv, kv, plan), kv, do)
-    o, lse = sla.prompt_forward(q, k, k, plan)
-    _, dk, dv = sla.prompt_backward(q, k, k, o, lse, do, plan)
+    o, lse, rest = sla.prompt_forward(q, k, k, plan, want_rest=True)
+    _, dk, dv = sla.prompt_backward(q, k, k, o, lse, do, plan, rest=rest)
     assert torch.equal(dkv, dk + dv)
     one = k[:, :1].float().requires_grad_(True)
     (d1,) = torch.autograd.grad(sla.prompt_attention(q, one.bfloat16().expand(-1, 2, -1), v, plan), one, do)
