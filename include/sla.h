@@ -435,9 +435,11 @@ typedef struct sla_rows {
 /* SLA_OK, or why these parameters are refused. */
 sla_status sla_prompt_validate(const sla_prompt_params* p);
 
-/* Bytes of the plan (0 for invalid parameters), and the plan itself. */
+/* Bytes to have ready for the plan (0 for invalid parameters), the plan itself, and
+ * the bytes of it that are used (the ones to copy). */
 size_t sla_prompt_plan_size(const sla_prompt_params* p);
 sla_status sla_prompt_plan(const sla_prompt_params* p, void* plan, size_t plan_bytes);
+size_t sla_prompt_plan_used(const void* plan);
 
 /* Bytes of device workspace of sla_prompt_forward (0: none needed; it is used
  * where few rows read long caches, whose keys are then split among blocks). */

@@ -16,7 +16,16 @@ fallback: if the compiled library is missing, load() raises.
     # SLA2's SoftTop-k router (first training stage)
     m, lam, pc, _ = sla.router_soft_topk(q, k, tau=0.01, params=p, want_pc=True)
 
-q, k, v: [B, H, N_pad, d] torch.bfloat16 CUDA tensors, N_pad = 64 * ceil(N / 64).
+    # queries and keys normalised per head and rotated on the way (three position axes)
+    table = sla.rope_table(128, sections=(22, 21, 21))
+    o = sla.attention(q, k, v, N=N, k_crit=25, qk_norm=(wq, wk), rotary=table, positions=grid)
+
+    # exact causal attention over packed prompts with grouped heads
+    plan = sla.prompt_plan([512, 77], Hq=32, Hkv=8, d=128)
+    o = sla.prompt_attention(q, k, v, plan)
+
+q, k, v: [B, H, N_pad, d] torch.bfloat16 CUDA tensors, N_pad = 64 * ceil(N / 64)
+(prompt_attention: packed tokens [T, H, d]).
 """
 from __future__ import annotations
 
@@ -41,7 +50,7 @@ EXPORTS = ("sla_abi_version", "sla_status_string", "sla_validate", "sla_workspac
            "sla_get_quantized", "sla_router_soft_topk", "sla_forward_train", "sla_backward_workspace_size",
            "sla_backward", "sla_check_wait_timeout",
            "sla_rope", "sla_qk_norm_rope", "sla_qk_norm_rope_backward_workspace_size", "sla_qk_norm_rope_backward",
-           "sla_prompt_validate", "sla_prompt_plan_size", "sla_prompt_plan", "sla_prompt_workspace_size",
+           "sla_prompt_validate", "sla_prompt_plan_size", "sla_prompt_plan", "sla_prompt_plan_used", "sla_prompt_workspace_size",
            "sla_prompt_forward", "sla_prompt_backward_workspace_size", "sla_prompt_backward")
 NOALLOC_WORKSPACE_BYTES = 32 << 20
 NUM_STAGES = 6
@@ -139,6 +148,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sla_prompt_validate": (i, [PP]),
         "sla_prompt_plan_size": (sz, [PP]),
         "sla_prompt_plan": (i, [PP, vp, sz]),
+        "sla_prompt_plan_used": (sz, [vp]),
         "sla_prompt_workspace_size": (sz, [vp]),
         "sla_prompt_forward": (i, [TP, TP, TP, TP, vp, vp, vp, sz, vp, vp, sz, vp]),
         "sla_prompt_backward_workspace_size": (sz, [vp]),
@@ -403,12 +413,26 @@ def backward(q, k, v, do, *, params: Params, saved: dict, fwd_workspace, want_pa
 
 def attention(q, k, v, *, N: Optional[int] = None, variant: str = "sla", k_crit: int, k_neg: int = 0,
               softmax_scale: float = 0.0, w_proj=None, proj_q=None, proj_k=None, alpha=None,
-              phi: str = "softmax"):
+              phi: str = "softmax", qk_norm=None, norm_eps: float = 1e-6, rotary=None, positions=None):
     """Differentiable SLA / SLA2 attention for PyTorch: the forward through
     sla_forward_train and, on .backward(), the gradients through sla_backward
     (mask held fixed) for q, k, v and, when they require grad, SLA's w_proj
-    and SLA2's alpha. Arguments as for forward(); every tensor on the GPU."""
+    and SLA2's alpha. Arguments as for forward(); every tensor on the GPU.
+
+    qk_norm = (wq, wk) normalises every query and key head first (qk_norm_rope; the
+    weights get gradients too), rotary = a rope_table() turns them by `positions`, both
+    in one pass over q and k."""
     import torch
+
+    if qk_norm is not None or rotary is not None:
+        from .rotary import qk_norm_rope as norm, rope as turn
+
+        if qk_norm is not None:
+            q, k = norm(q, k, *qk_norm, rotary, positions, eps=norm_eps, N=N)
+        else:
+            q, k = turn(q, rotary, positions, N=N), turn(k, rotary, positions, N=N)
+    elif positions is not None:
+        raise ValueError("positions without a rotary table")
 
     class _SLAFunction(torch.autograd.Function):
         @staticmethod

@@ -51,9 +51,16 @@ int key_blocks(const sla_prompt_params& p, int lq, int lk, int last_token) {
   return int((std::max(0LL, keys) + kPromptTile - 1) / kPromptTile);
 }
 
+long long row_item_count(const sla_prompt_params& p, int per) {
+  long long n = 0;
+  for (int s = 0; s < p.n_seq; ++s) n += ((long long)p.len_q[s] + per - 1) / per * p.Hkv;
+  return n;
+}
+
 // Items of `per` tokens, all key blocks each.
 std::vector<PromptItem> row_items(const sla_prompt_params& p, int per) {
   std::vector<PromptItem> out;
+  out.reserve(size_t(row_item_count(p, per)));
   int q0 = 0, k0 = 0;
   for (int s = 0; s < p.n_seq; ++s) {
     const int lq = p.len_q[s], lk = p.len_k ? p.len_k[s] : lq;
@@ -74,6 +81,20 @@ std::vector<PromptItem> row_items(const sla_prompt_params& p, int per) {
     k0 += lk;
   }
   return out;
+}
+
+// Longest first, equals in their order: a counting sort (plans are made per batch, and
+// comparison sorts of their thousands of items were half of the time).
+template <typename T, typename Length>
+void longest_first(std::vector<T>& items, Length length) {
+  int most = 0;
+  for (const T& it : items) most = std::max(most, length(it));
+  std::vector<int> at(size_t(most) + 2, 0);
+  for (const T& it : items) ++at[size_t(most - length(it)) + 1];
+  for (size_t i = 1; i < at.size(); ++i) at[i] += at[i - 1];
+  std::vector<T> out(items.size());
+  for (const T& it : items) out[size_t(at[size_t(most - length(it))]++)] = it;
+  items.swap(out);
 }
 
 // Time at which the last of `places` ends, items dispatched longest first.
@@ -148,6 +169,12 @@ Lists make_lists(const sla_prompt_params& p) {
   std::vector<PromptItem> base;
   for (int tiles = longest <= tpt ? 1 : 2; tiles >= 1; --tiles) {
     std::vector<PromptItem> items = row_items(p, tiles * tpt);
+    if (base.empty() && items.size() >= 4 * kPromptSms && (tiles == 1 || items.size() >= 8 * kPromptSms)) {
+      // rounds enough: neither splits nor smaller items can be better
+      base = std::move(items);
+      L.tiles = tiles;
+      break;
+    }
     std::vector<int> chunks = {0};
     if (items.size() < 4 * kPromptSms) {
       std::vector<int> lengths;
@@ -180,8 +207,7 @@ Lists make_lists(const sla_prompt_params& p) {
       L.items.push_back(part);
     }
   }
-  auto longer = [](const PromptItem& a, const PromptItem& b) { return a.b1 - a.b0 > b.b1 - b.b0; };
-  std::stable_sort(L.items.begin(), L.items.end(), longer);
+  longest_first(L.items, [](const PromptItem& it) { return it.b1 - it.b0; });
   if (p.backward) add_backward(p, L);
   return L;
 }
@@ -190,11 +216,16 @@ Lists make_lists(const sla_prompt_params& p) {
 // tiles are split where few key tiles see many of them.
 void add_backward(const sla_prompt_params& p, Lists& L) {
   const int G = p.Hq / p.Hkv, tpt = kPromptTile / G;
-  auto longer = [](const PromptItem& a, const PromptItem& b) { return a.b1 > b.b1; };
   double best = 0.0;
   for (int tiles = 2; tiles >= 1; --tiles) {
+    const long long count = row_item_count(p, tiles * tpt);
+    if (tiles == 1 && count >= 8 * kPromptSms) break;
     std::vector<PromptItem> rows = row_items(p, tiles * tpt);
-    if (tiles == 1 && rows.size() >= 8 * kPromptSms) break;
+    if (tiles == 2 && count >= 4 * kPromptSms) {  // rounds enough for two tiles each
+      L.rows = std::move(rows);
+      L.row_tiles = 2;
+      break;
+    }
     const double c = split_cost(rows, 0, 2, 1.0) * (tiles == 2 ? 1.0 : 0.8);  // one CTA per SM either way
     if (tiles == 2 || c < best) {
       best = c;
@@ -202,7 +233,7 @@ void add_backward(const sla_prompt_params& p, Lists& L) {
       L.row_tiles = tiles;
     }
   }
-  std::stable_sort(L.rows.begin(), L.rows.end(), longer);
+  longest_first(L.rows, [](const PromptItem& it) { return it.b1; });
 
   std::vector<PromptKeys> base;
   int q0 = 0, k0 = 0;
@@ -237,6 +268,7 @@ void add_backward(const sla_prompt_params& p, Lists& L) {
   int chunk = 0;
   best = -1.0;
   for (int c : chunks) {
+    if (chunks.size() == 1) break;
     std::vector<double> cost;
     bool any = false;
     for (const PromptKeys& it : base) {
@@ -266,8 +298,7 @@ void add_backward(const sla_prompt_params& p, Lists& L) {
       L.keys.push_back(part);
     }
   }
-  std::stable_sort(L.keys.begin(), L.keys.end(),
-                   [](const PromptKeys& a, const PromptKeys& b) { return a.t1 - a.t0 > b.t1 - b.t0; });
+  longest_first(L.keys, [](const PromptKeys& it) { return it.t1 - it.t0; });
 }
 
 size_t layout(const sla_prompt_params& p, const Lists& L, PromptPlan* h) {
@@ -357,8 +388,26 @@ sla_status sla_prompt_validate(const sla_prompt_params* p) { return check_params
 
 size_t sla_prompt_plan_size(const sla_prompt_params* p) {
   if (check_params(p) != SLA_OK) return 0;
-  PromptPlan h;
-  return layout(*p, make_lists(*p), &h);
+  // an upper bound: every list at its longest (a split makes at most three rounds of pieces)
+  const int tpt = kPromptTile / (p->Hq / p->Hkv);
+  const size_t rows = size_t(row_item_count(*p, tpt)), parts = 6 * kPromptSms;
+  size_t n = 6 * 256 + align256(sizeof(PromptPlan)) + std::max(rows, parts) * sizeof(PromptItem) +
+             std::min(rows, parts) * sizeof(PromptJoin);
+  if (p->backward) {
+    size_t keys = 0;
+    for (int i = 0; i < p->n_seq; ++i) {
+      const size_t lk = size_t(p->len_k ? p->len_k[i] : p->len_q[i]);
+      keys += (lk + kPromptTile - 1) / kPromptTile * p->Hkv;
+    }
+    n += std::max(keys, parts) * sizeof(PromptKeys) + std::min(keys, parts) * sizeof(PromptKeysJoin) +
+         rows * sizeof(PromptItem);
+  }
+  return align256(n);
+}
+
+size_t sla_prompt_plan_used(const void* plan) {
+  const PromptPlan* p = plan_of(plan, ~size_t(0));
+  return p == nullptr ? 0 : size_t(p->total);
 }
 
 sla_status sla_prompt_plan(const sla_prompt_params* p, void* plan, size_t plan_bytes) {

@@ -67,15 +67,13 @@ def prompt_plan(lens_q: Sequence[int], lens_k: Optional[Sequence[int]] = None, *
     st = lib.sla_prompt_validate(p)
     if st:
         raise SLAError(st, "sla_prompt_plan")
-    size = lib.sla_prompt_plan_size(p)
-    host = ctypes.create_string_buffer(size + 8)
-    at = (ctypes.addressof(host) + 7) // 8 * 8 - ctypes.addressof(host)
-    host = (ctypes.c_char * size).from_buffer(host, at)  # 8-byte aligned
-    st = lib.sla_prompt_plan(p, host, size)
+    words = (ctypes.c_longlong * (lib.sla_prompt_plan_size(p) // 8))()  # 8-byte aligned
+    st = lib.sla_prompt_plan(p, words, ctypes.sizeof(words))
     if st:
         raise SLAError(st, "sla_prompt_plan")
-    return PromptPlan(host, torch.frombuffer(bytearray(host.raw), dtype=torch.uint8).to(device), lens_q, lens_k,
-                      int(Hq), int(Hkv), int(d), bool(causal), grad)
+    host = (ctypes.c_char * lib.sla_prompt_plan_used(words)).from_buffer(words)
+    return PromptPlan(host, torch.frombuffer(host, dtype=torch.uint8).to(device, copy=True), lens_q, lens_k, int(Hq),
+                      int(Hkv), int(d), bool(causal), grad)
 
 
 def prompt_forward(q, k, v, plan: PromptPlan, *, out=None, want_lse: bool = True, want_rest: bool = False,

@@ -66,7 +66,9 @@ def test_plan_covers_every_row_and_key_once(lib, lq, lk, Hq, Hkv, causal):
     G = Hq // Hkv
     tpt = 128 // G
     assert (h.status, h.Hq, h.Hkv, h.G, h.Tq, h.Tk) == (0, Hq, Hkv, G, sum(lq), sum(lk))
-    assert h.total == len(plan.host.raw)
+    lens = [(ctypes.c_int32 * len(x))(*x) for x in (lq, lk)]
+    assert h.total == len(plan.host.raw) <= lib.sla_prompt_plan_size(sla.PromptParams(
+        len(lq), ctypes.addressof(lens[0]), ctypes.addressof(lens[1]), Hq, Hkv, 64, int(causal), 1, 0.0))
 
     def seen_blocks(pos):
         return ceil(max(0, min(pos + 1, lk_s)), 128) if causal else ceil(lk_s, 128)
@@ -173,10 +175,14 @@ def test_plan_argument_errors(lib):
     p = sla.PromptParams(**ok)
     size = lib.sla_prompt_plan_size(p)
     buf = (ctypes.c_longlong * (size // 8 + 1))()
+    assert lib.sla_prompt_plan_used(None) == 0 == lib.sla_prompt_plan_used(buf)  # no plan there yet
     assert lib.sla_prompt_plan(p, None, size) == sla.SLA_ERR_INVALID_ARG
     assert lib.sla_prompt_plan(p, ctypes.addressof(buf) + 4, size) == sla.SLA_ERR_ALIGNMENT
-    assert lib.sla_prompt_plan(p, buf, size - 1) == sla.SLA_ERR_WORKSPACE
     assert lib.sla_prompt_plan(p, buf, size) == sla.SLA_OK
+    used = lib.sla_prompt_plan_used(buf)
+    assert 0 < used <= size
+    assert lib.sla_prompt_plan(p, buf, used - 1) == sla.SLA_ERR_WORKSPACE
+    assert lib.sla_prompt_plan(p, buf, used) == sla.SLA_OK
 
 
 def rows(base=0x10000, row=512, head=64):
