@@ -92,7 +92,7 @@ namespace {
 template <int D>
 struct KeyCfg {
   static constexpr int kTileBytes = kSub * (D / 64);
-  static constexpr int kStages = 2;
+  static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int oK = 0, oV = kTileBytes, oQ = 2 * kTileBytes;
   static constexpr int oG = oQ + kStages * kTileBytes;
   // the extra K steps: [2 column octets][128 rows][8] bf16, not swizzled
@@ -101,10 +101,16 @@ struct KeyCfg {
   static constexpr int oL = oOne + kStep;                 // B of S and of dP, per stage
   static constexpr int kBytes = oL + kStages * 2 * kStep;
   static constexpr int kSmem = kBytes + 1024;
-  static constexpr int kFmaPairs = 2;  // of every 8 pairs of exponentials, formed on the FMA units
-  static constexpr int cS = 0, cP = 128, cV = 256, cK = 256 + D;  // TMEM columns
+  // Of every 8 pairs of exponentials, formed on the FMA units. Measured, backward of 14693
+  // tokens, 16 + 4 heads, d = 128: none 1032 us, two 1012, three 997, four 1020; of 8192
+  // tokens, 16 heads, d = 64: none 575 us, two 597, three 604.
+  static constexpr int kFmaPairs = D == 64 ? 0 : 3;
+  // TMEM columns. At d = 64 there is room for a second S, so that the next tile's S is
+  // formed while this one's P is in use (a tile takes 2280 clocks instead of 2620).
+  static constexpr bool kTwoS = D == 64;
+  static constexpr int cS = 0, cP = 128, cV = 256, cK = 256 + D, cS1 = kTwoS ? 384 : 0;
 };
-enum { kbKV = 0, kbS, kbP, kbPr, kbDr, kbDone, kbL0, kbL1, kbQ };  // then Q, dO full / empty of every stage
+enum { kbKV = 0, kbS0, kbS1, kbP, kbPr, kbDr, kbDone, kbQ };  // then Q full / empty, dO full / empty, (lse, D) full of every stage
 
 }  // namespace
 
@@ -115,7 +121,7 @@ __global__ void __launch_bounds__(320, 1)
   constexpr int ST = C::kStages;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t bars[kbQ + 4 * ST];
+  __shared__ __align__(8) uint64_t bars[kbQ + 5 * ST];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -146,11 +152,16 @@ __global__ void __launch_bounds__(320, 1)
   auto qempty = [&](int i) { return kbQ + ST + i % ST; };
   auto gfull = [&](int i) { return kbQ + 2 * ST + i % ST; };
   auto gempty = [&](int i) { return kbQ + 3 * ST + i % ST; };
+  auto lfull = [&](int i) { return kbQ + 4 * ST + i % ST; };
+  // S of tile i: its barrier (with two S, one each), the phase of it, its columns
+  auto s_bar = [&](int i) { return C::kTwoS ? kbS0 + (i & 1) : kbS0; };
+  auto s_phase = [&](int i) { return uint32_t(C::kTwoS ? i >> 1 : i) & 1; };
+  auto s_col = [&](int i) { return C::kTwoS && (i & 1) ? C::cS1 : C::cS; };
   auto phase = [&](int i) { return uint32_t(i / ST) & 1; };
 
   if (threadIdx.x == 0) {
     abort_sh = 0;
-    for (int i = 0; i < kbQ + 4 * ST; ++i) mbar_init(bar(i), i == kbPr || i == kbDr ? 256 : i == kbL0 || i == kbL1 ? 32 : 1);
+    for (int i = 0; i < kbQ + 5 * ST; ++i) mbar_init(bar(i), i == kbPr || i == kbDr ? 256 : i >= kbQ + 4 * ST ? 32 : 1);
     fence_barrier_init();
   }
   for (int x = threadIdx.x; x < (1 + 2 * ST) * (C::kStep / 16); x += 320) {
@@ -219,7 +230,7 @@ __global__ void __launch_bounds__(320, 1)
           *reinterpret_cast<uint4*>(to + C::kStep + r * 16) = three_bf16(-next[j].y);
         }
         fence_async_smem();
-        mbar_arrive(bar(i % ST == 0 ? kbL0 : kbL1));
+        mbar_arrive(bar(lfull(i)));
         fetch(i + 1);
         if (!wait_w(gempty(i), phase(i) ^ 1)) break;
         if (lane == 0) {
@@ -261,12 +272,12 @@ __global__ void __launch_bounds__(320, 1)
       mma_bf16(tb + col, sdesc(sb + C::oOne, 2048, 128, 0), sdesc(sb + ext, 2048, 128, 0), idS, 1);
     };
     auto issue_s = [&](int i) {
-      wait_w(i % ST == 0 ? kbL0 : kbL1, phase(i));
+      wait_w(lfull(i), phase(i));
       wait_w(qfull(i), phase(i));
       clear_tail(i, C::oQ);
       tc_fence_after();
-      issue_wide(C::cS, C::oK, C::oQ + (i % ST) * C::kTileBytes, C::oL + (i % ST) * 2 * C::kStep);
-      mma_commit(bar(kbS));
+      issue_wide(s_col(i), C::oK, C::oQ + (i % ST) * C::kTileBytes, C::oL + (i % ST) * 2 * C::kStep);
+      mma_commit(bar(s_bar(i)));
     };
     auto issue_p = [&](int i) {
       wait_w(gfull(i), phase(i));
@@ -288,11 +299,12 @@ __global__ void __launch_bounds__(320, 1)
       issue_p(0);
     }
     for (int i = 0; i < n; ++i) {
+      if (C::kTwoS && i + 1 < n) issue_s(i + 1);
       wait_w(kbPr, i & 1);
       tc_fence_after();
-      issue_acc(C::cV, C::cS, sb + C::oG + (i % ST) * C::kTileBytes, i == 0);
+      issue_acc(C::cV, s_col(i), sb + C::oG + (i % ST) * C::kTileBytes, i == 0);
       mma_commit(bar(gempty(i)));
-      if (i + 1 < n) issue_s(i + 1);
+      if (!C::kTwoS && i + 1 < n) issue_s(i + 1);
       wait_w(kbDr, i & 1);
       tc_fence_after();
       issue_acc(C::cK, C::cP, sb + C::oQ + (i % ST) * C::kTileBytes, i == 0);
@@ -307,7 +319,7 @@ __global__ void __launch_bounds__(320, 1)
     const int key = it.block * 128 + r;                 // in the sequence
     const bool live = key < it.lk;
     const uint32_t tq = tb + (uint32_t(32 * (warp & 3)) << 16);
-    const uint32_t tS = tq + C::cS + half * 64, tP = tq + C::cP + half * 64;
+    const uint32_t tP = tq + C::cP + half * 64;
     const uint64_t c2 = two(a.scale_log2, a.scale_log2);
     for (int i = 0; i < n; ++i) {
       const int tok = (it.t0 + i) * a.tpt;
@@ -316,7 +328,8 @@ __global__ void __launch_bounds__(320, 1)
       const int lo = int(max(0LL, min(128LL, first * a.G))) - half * 64;
       const int hi = min(rows, (it.lq - tok) * a.G) - half * 64;
       const bool masked = lo > 0 || hi < 64;
-      wait_w(kbS, i & 1);
+      const uint32_t tS = tq + s_col(i) + half * 64;
+      wait_w(s_bar(i), s_phase(i));
       tc_fence_after();
       float p[64];
       tmem_ld32(tS, *reinterpret_cast<float(*)[32]>(&p[0]));
@@ -632,6 +645,7 @@ __global__ void __launch_bounds__(384, 1)
     const long long token = (long long)it.q0 + tok;
     float2 w = make_float2(0.0f, 0.0f);
     if (live) w = a.ld[it.head * (a.Tq * a.G) + token * a.G + g];
+    const uint64_t c2 = two(c, c), lse2 = two(-w.x, -w.x);
     for (int i = 0; i < nb; ++i) {
       const int seen = limit - (nb - 1 - i) * 128;
       const bool masked = (nb - i) * 128 > warp_limit;
@@ -644,7 +658,11 @@ __global__ void __launch_bounds__(384, 1)
       tc_fence_before();
       mbar_arrive(bar(rbR0 + t));
 #pragma unroll
-      for (int j = 0; j < 128; ++j) p[j] = ex2(fmaf(p[j], c, -w.x));
+      for (int j = 0; j < 128; j += 2) {
+        untwo(fma2(two(p[j], p[j + 1]), c2, lse2), p[j], p[j + 1]);
+        p[j] = ex2(p[j]);
+        p[j + 1] = ex2(p[j + 1]);
+      }
       wait_w(rbP0 + t, i & 1);
       tc_fence_after();
 #pragma unroll
