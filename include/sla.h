@@ -424,7 +424,7 @@ typedef struct sla_prompt_params {
   int d;                 /* 64 or 128 */
   int causal;            /* 0 or 1 */
   int backward;          /* 1: the plan also lists sla_prompt_backward's items */
-  float softmax_scale;   /* 0 selects 1/sqrt(d) */
+  float softmax_scale;   /* 0 selects 1/sqrt(d); else at least 1e-30 */
 } sla_prompt_params;
 
 typedef struct sla_rows {

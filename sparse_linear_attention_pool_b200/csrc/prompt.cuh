@@ -8,6 +8,7 @@ namespace sla {
 
 constexpr int kPromptTile = 128;  // packed query rows and keys per tile
 constexpr int kPromptSms = 148;
+constexpr int kPromptFew = 32;   // rows of an item that the single-token variant takes
 
 // A packed query tile holds tpt = 128 / G whole tokens: row t G + g is token t,
 // query head (key head) G + g. The G heads that share a key head so share its
@@ -47,6 +48,7 @@ struct PromptPlan {
   int n_seq, Hq, Hkv, G, d, causal;
   float scale;
   int tiles;   // query tiles per forward item (1 or 2)
+  int few;     // forward items have at most kPromptFew rows
   long long Tq, Tk;
   int n_items, n_joins, n_slots, join_rows;  // join_rows: rows of a joined item up to its last live one
   // backward (all 0 in a plan without it)

@@ -18,11 +18,14 @@ using namespace sla;
 
 namespace {
 
+constexpr long long kMostItems = 1LL << 22;
+
 sla_status check_params(const sla_prompt_params* p) {
   if (p == nullptr || p->n_seq < 1 || p->len_q == nullptr) return SLA_ERR_INVALID_ARG;
   if (p->Hq < 1 || p->Hkv < 1 || p->Hq % p->Hkv != 0) return SLA_ERR_INVALID_ARG;
   if ((p->causal != 0 && p->causal != 1) || (p->backward != 0 && p->backward != 1)) return SLA_ERR_INVALID_ARG;
-  if (!(p->softmax_scale >= 0.0f) || isinf(p->softmax_scale)) return SLA_ERR_INVALID_ARG;
+  // 0: the default; tiny ones would make the backward's lse / scale overflow
+  if (!(p->softmax_scale == 0.0f || p->softmax_scale >= 1e-30f) || isinf(p->softmax_scale)) return SLA_ERR_INVALID_ARG;
   if (p->d != 64 && p->d != 128) return SLA_ERR_UNSUPPORTED;
   if (p->Hq / p->Hkv > 128 || p->Hq > 65535) return SLA_ERR_UNSUPPORTED;
   long long tq = 0, tk = 0;
@@ -35,6 +38,14 @@ sla_status check_params(const sla_prompt_params* p) {
   if (tq < 1) return SLA_ERR_INVALID_ARG;
   // rows, positions and tile ends are 32-bit in the kernels
   if (tq > 0x7fffffffLL - 1024 || tk > 0x7fffffffLL - 1024) return SLA_ERR_UNSUPPORTED;
+  // the plan's lists: at most 2^22 items each (200 MB)
+  const int tpt = kPromptTile / (p->Hq / p->Hkv);
+  long long rows = 0, keys = 0;
+  for (int i = 0; i < p->n_seq; ++i) {
+    rows += ((long long)p->len_q[i] + tpt - 1) / tpt;
+    keys += ((long long)(p->len_k ? p->len_k[i] : p->len_q[i]) + kPromptTile - 1) / kPromptTile;
+  }
+  if (rows * p->Hkv > kMostItems || (p->backward && keys * p->Hkv > kMostItems)) return SLA_ERR_UNSUPPORTED;
   return SLA_OK;
 }
 
@@ -135,17 +146,21 @@ int chunk_for(const std::vector<int>& lengths, int most) {
 
 // Costs in units of one key block of a two-tile item, the only one on its SM.
 constexpr double kItemCost = 3.0;  // start, first loads and the store
-constexpr double kOneTile = 1.0;   // a step of a one-tile item, two of which share an SM
-constexpr double kAlone = 0.7;     // and of one that has its SM to itself
 constexpr double kJoinCost = 3.0;  // the second launch
+// A step of a one-tile item, two of which share an SM, and of one that has its SM to
+// itself. At d = 128 the second copy of the keys costs bandwidth to shared memory
+// (18832 causal tokens, 2 heads: 200 us as one-tile items, 174 as two-tile ones); at
+// d = 64 the exponentials bound both (16384 tokens, 16 heads: 669 and 643 us; 8192 full
+// ones, whose two-tile items leave half of their last round idle: 349 and 418).
+double one_tile_step(int d, bool shared) { return shared ? (d == 128 ? 1.4 : 0.97) : (d == 128 ? 0.9 : 0.7); }
 
 // full_rows: how full of live rows the tiles are
-double split_cost(const std::vector<PromptItem>& items, int chunk, int tiles, double full_rows) {
+double split_cost(const std::vector<PromptItem>& items, int chunk, int tiles, double full_rows, int d) {
   std::vector<double> cost;
   size_t parts = 0;
   for (const PromptItem& it : items) parts += pieces(it.b1, chunk);
   const bool shared = tiles == 1 && parts > size_t(kPromptSms);
-  const double step = tiles == 2 ? 1.0 : shared ? kOneTile : kAlone;
+  const double step = tiles == 2 ? 1.0 : one_tile_step(d, shared);
   double joins = 0.0;  // rows of partial results, in tiles: written and read once more in float32
   for (const PromptItem& it : items) {
     const int n = pieces(it.b1, chunk);
@@ -182,7 +197,7 @@ Lists make_lists(const sla_prompt_params& p) {
       for (int rounds = 1; rounds <= 3; ++rounds) chunks.push_back(chunk_for(lengths, rounds * kPromptSms * (3 - tiles)));
     }
     for (int chunk : chunks) {
-      const double c = split_cost(items, chunk, tiles, std::min(1.0, double(longest) / tpt));
+      const double c = split_cost(items, chunk, tiles, std::min(1.0, double(longest) / tpt), p.d);
       if (base.empty() || c < best) {
         best = c;
         best_chunk = chunk;
@@ -226,7 +241,7 @@ void add_backward(const sla_prompt_params& p, Lists& L) {
       L.row_tiles = 2;
       break;
     }
-    const double c = split_cost(rows, 0, 2, 1.0) * (tiles == 2 ? 1.0 : 0.8);  // one CTA per SM either way
+    const double c = split_cost(rows, 0, 2, 1.0, p.d) * (tiles == 2 ? 1.0 : 0.8);  // one CTA per SM either way
     if (tiles == 2 || c < best) {
       best = c;
       L.rows = std::move(rows);
@@ -312,6 +327,9 @@ size_t layout(const sla_prompt_params& p, const Lists& L, PromptPlan* h) {
   h->causal = p.causal;
   h->scale = p.softmax_scale > 0.0f ? p.softmax_scale : 1.0f / sqrtf(float(p.d));
   h->tiles = L.tiles;
+  int longest = 0;
+  for (int i = 0; i < p.n_seq; ++i) longest = std::max(longest, p.len_q[i]);
+  h->few = L.tiles == 1 && (long long)longest * h->G <= kPromptFew;
   for (int i = 0; i < p.n_seq; ++i) {
     h->Tq += p.len_q[i];
     h->Tk += p.len_k ? p.len_k[i] : p.len_q[i];
@@ -341,6 +359,23 @@ size_t layout(const sla_prompt_params& p, const Lists& L, PromptPlan* h) {
   h->rows = take(L.rows.size() * sizeof(PromptItem));
   h->total = off;
   return off;
+}
+
+sla_status write_plan(const sla_prompt_params& p, unsigned char* out, size_t bytes) {
+  const Lists L = make_lists(p);
+  PromptPlan h;
+  if (bytes < layout(p, L, &h)) return SLA_ERR_WORKSPACE;
+  memset(out, 0, h.total);
+  memcpy(out, &h, sizeof(h));
+  auto put = [&](size_t at, const void* src, size_t size) {
+    if (size) memcpy(out + at, src, size);
+  };
+  put(h.items, L.items.data(), L.items.size() * sizeof(PromptItem));
+  put(h.joins, L.joins.data(), L.joins.size() * sizeof(PromptJoin));
+  put(h.keys, L.keys.data(), L.keys.size() * sizeof(PromptKeys));
+  put(h.kjoins, L.kjoins.data(), L.kjoins.size() * sizeof(PromptKeysJoin));
+  put(h.rows, L.rows.data(), L.rows.size() * sizeof(PromptItem));
+  return SLA_OK;
 }
 
 const PromptPlan* plan_of(const void* plan, size_t bytes) {
@@ -415,21 +450,11 @@ sla_status sla_prompt_plan(const sla_prompt_params* p, void* plan, size_t plan_b
   if (st != SLA_OK) return st;
   if (plan == nullptr) return SLA_ERR_INVALID_ARG;
   if (!aligned(plan, 8)) return SLA_ERR_ALIGNMENT;
-  const Lists L = make_lists(*p);
-  PromptPlan h;
-  if (plan_bytes < layout(*p, L, &h)) return SLA_ERR_WORKSPACE;
-  unsigned char* out = static_cast<unsigned char*>(plan);
-  memset(out, 0, h.total);
-  memcpy(out, &h, sizeof(h));
-  auto put = [&](size_t at, const void* src, size_t bytes) {
-    if (bytes) memcpy(out + at, src, bytes);
-  };
-  put(h.items, L.items.data(), L.items.size() * sizeof(PromptItem));
-  put(h.joins, L.joins.data(), L.joins.size() * sizeof(PromptJoin));
-  put(h.keys, L.keys.data(), L.keys.size() * sizeof(PromptKeys));
-  put(h.kjoins, L.kjoins.data(), L.kjoins.size() * sizeof(PromptKeysJoin));
-  put(h.rows, L.rows.data(), L.rows.size() * sizeof(PromptItem));
-  return SLA_OK;
+  try {  // the lists are host memory: running out of it must not pass this C boundary as an exception
+    return write_plan(*p, static_cast<unsigned char*>(plan), plan_bytes);
+  } catch (...) {
+    return SLA_ERR_WORKSPACE;
+  }
 }
 
 size_t sla_prompt_workspace_size(const void* plan) {

@@ -36,7 +36,7 @@ struct PromptDev {
   long long o_row, o_head;
   __nv_bfloat16* rest;
   float *lse, *part, *part_lse;
-  int Hq, G, tpt, causal, tiles;
+  int Hq, G, tpt, box, causal, tiles;  // box: tokens that a copy of Q brings
   long long Tq, Tk;
   float scale, scale_log2;
 };
@@ -44,7 +44,7 @@ struct PromptDev {
 namespace {
 
 
-template <int D, int TILES>
+template <int D, int TILES, bool FEW>
 struct FwdCfg {
   static constexpr int kSub = 128 * 128;             // 128 rows x 128 bytes (64 columns)
   static constexpr int kTileBytes = kSub * (D / 64);  // 128 x D bf16
@@ -52,9 +52,13 @@ struct FwdCfg {
   // give up registers). One tile: two CTAs per SM, each with half the ring and TMEM.
   static constexpr int kSoft = 4 * TILES, kThreads = TILES == 2 ? 384 : 192;
   static constexpr int kCtas = TILES == 2 ? 1 : 2;
-  static constexpr int kStages = D == 128 ? (TILES == 2 ? 4 : 2) : (TILES == 2 ? 8 : 5);  // K and V tiles in the ring
+  // FEW: no item has more than 32 rows (single tokens over caches): Q takes 32 rows of
+  // shared memory and the ring one tile more, for the loads are what counts. The products
+  // read 96 more rows from what follows, which reach only the TMEM lanes of rows that are not there.
+  static constexpr int kQSub = FEW ? 32 * 128 : kSub;  // 64 columns of Q
+  static constexpr int kStages = D == 128 ? (TILES == 2 ? 4 : FEW ? 3 : 2) : (TILES == 2 ? 8 : FEW ? 6 : 5);
   static constexpr int oQ = 0;
-  static constexpr int oKV = TILES * kTileBytes;
+  static constexpr int oKV = TILES * kQSub * (D / 64);
   static constexpr int kBytes = oKV + kStages * kTileBytes;
   static constexpr int kSmem = kBytes + 1024;
   // Of every 8 pairs of exponents, this many are formed on the FMA units: the special
@@ -77,10 +81,10 @@ enum { bQ0 = 0, bQ1, bS0, bS1, bP0, bP1, bR0, bR1, bX0, bX1, bO0, bO1, bDone, bK
 
 }  // namespace
 
-template <int D, int TILES>
-__global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, FwdCfg<D, TILES>::kCtas)
+template <int D, int TILES, bool FEW>
+__global__ void __launch_bounds__(FwdCfg<D, TILES, FEW>::kThreads, FwdCfg<D, TILES, FEW>::kCtas)
     prompt_fwd_kernel(const __grid_constant__ PromptMaps maps, const PromptDev a) {
-  using C = FwdCfg<D, TILES>;
+  using C = FwdCfg<D, TILES, FEW>;
   constexpr int ST = C::kStages;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -91,7 +95,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, FwdCfg<D, TILES>::
   int* status = reinterpret_cast<int*>(a.plan_dev);
   const PromptItem it = a.items[blockIdx.x];
   if (it.q0 < 0 || it.nq < 1 || it.k0 < 0 || it.lk < 0 || it.q0 + (long long)it.nq > a.Tq ||
-      it.k0 + (long long)it.lk > a.Tk || it.nq > TILES * a.tpt || it.b0 < 0 || it.head < 0) {
+      it.k0 + (long long)it.lk > a.Tk || it.nq > TILES * a.tpt || (FEW && it.nq > a.box) || it.b0 < 0 || it.head < 0) {
     if (threadIdx.x == 0) atomicExch(status, kDevBadIndex);
     return;
   }
@@ -141,12 +145,12 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, FwdCfg<D, TILES>::
   if (warp == C::kSoft) {
     if (TILES == 2) reg_dec<40>();
     if (lane == 0 && n > 0) {
-      const int rows = a.G * a.tpt;
+      const int rows = a.G * a.box;
       for (int t = 0; t < TILES; ++t) {
         if ((t == 0 ? nb0 : nb1) <= it.b0) continue;
         mbar_expect_tx(bar(bQ0 + t), rows * D * 2);
         for (int s = 0; s < D / 64; ++s)
-          tma_load_4d(sb + C::oQ + t * C::kTileBytes + s * C::kSub, &maps.q, bar(bQ0 + t), s * 64, 0,
+          tma_load_4d(sb + C::oQ + t * C::kTileBytes + s * C::kQSub, &maps.q, bar(bQ0 + t), s * 64, 0,
                       it.q0 + t * a.tpt, it.head);
       }
       int issued = 0;
@@ -177,8 +181,8 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, FwdCfg<D, TILES>::
       const uint32_t sq = sb + C::oQ + t * C::kTileBytes, sk = sb + C::oKV + (k_pos(s) % ST) * C::kTileBytes;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        const uint32_t o = (k >> 2) * C::kSub + (k & 3) * 32;
-        mma_bf16(tb + t * 128, sdesc(sq + o, 16, 1024), sdesc(sk + o, 16, 1024), idS, k > 0);
+        mma_bf16(tb + t * 128, sdesc(sq + (k >> 2) * C::kQSub + (k & 3) * 32, 16, 1024),
+                 sdesc(sk + (k >> 2) * C::kSub + (k & 3) * 32, 16, 1024), idS, k > 0);
       }
       mma_commit(bar(bS0 + t));
     };
@@ -276,10 +280,21 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, FwdCfg<D, TILES>::
     const float c = a.scale_log2;
     const float slack = 8.0f / c;
     float m = -INFINITY, l = 0.0f;
+    const bool idle = !__any_sync(0xffffffffu, live);  // none of the warp's rows is there
     for (int i = 0; i < steps; ++i) {
       const int key0 = (nb - 1 - i) * 128;
       wait_w(bS0 + t, i & 1);
       tc_fence_after();
+      if (idle) {  // whatever its P holds reaches no row that is
+        if (C::kApart) {
+          mbar_arrive(bar(bX0 + t));
+          if (i > 0) wait_w(bO0 + t, (i - 1) & 1);  // not a block ahead of the other warps' P
+        } else {
+          mbar_arrive(bar(bP0 + t));
+        }
+        mbar_arrive(bar(bR0 + t));
+        continue;
+      }
       float s[128];
 #pragma unroll
       for (int j = 0; j < 4; ++j) tmem_ld32(tS + 32 * j, *reinterpret_cast<float(*)[32]>(&s[32 * j]));
@@ -478,16 +493,16 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const PromptDev a) {
 
 namespace {
 
-template <int D, int TILES>
+template <int D, int TILES, bool FEW>
 cudaError_t set_up() {
-  return cudaFuncSetAttribute(prompt_fwd_kernel<D, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              FwdCfg<D, TILES>::kSmem);
+  return cudaFuncSetAttribute(prompt_fwd_kernel<D, TILES, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              FwdCfg<D, TILES, FEW>::kSmem);
 }
 
-template <int D, int TILES>
+template <int D, int TILES, bool FEW>
 cudaError_t launch_d(const PromptArgs& a, const PromptMaps& maps, const PromptDev& v, cudaStream_t s) {
-  using C = FwdCfg<D, TILES>;
-  prompt_fwd_kernel<D, TILES><<<a.plan->n_items, C::kThreads, C::kSmem, s>>>(maps, v);
+  using C = FwdCfg<D, TILES, FEW>;
+  prompt_fwd_kernel<D, TILES, FEW><<<a.plan->n_items, C::kThreads, C::kSmem, s>>>(maps, v);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.plan->n_joins == 0) return e;
   cudaLaunchAttribute attr{};
@@ -507,8 +522,9 @@ cudaError_t launch_d(const PromptArgs& a, const PromptMaps& maps, const PromptDe
 cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s) {
   const PromptPlan& p = *a.plan;
   // first, for it makes the device's context current in this thread, which the tensor maps need
-  const bool two = p.tiles == 2;
-  const cudaError_t e = p.d == 128 ? (two ? set_up<128, 2>() : set_up<128, 1>()) : (two ? set_up<64, 2>() : set_up<64, 1>());
+  const bool two = p.tiles == 2, few = p.few != 0;
+  const cudaError_t e = p.d == 128 ? (two ? set_up<128, 2, false>() : few ? set_up<128, 1, true>() : set_up<128, 1, false>())
+                                   : (two ? set_up<64, 2, false>() : few ? set_up<64, 1, true>() : set_up<64, 1, false>());
   if (e != cudaSuccess) return e;
   PromptMaps maps;
   memset(&maps, 0, sizeof(maps));
@@ -526,17 +542,23 @@ cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s) {
   v.Hq = p.Hq;
   v.G = p.G;
   v.tpt = kPromptTile / p.G;
+  v.box = p.few ? kPromptFew / p.G : v.tpt;
   v.causal = p.causal;
   v.tiles = p.tiles;
   v.Tq = p.Tq;
   v.Tk = p.Tk;
   v.scale = p.scale;
   v.scale_log2 = p.scale * kLog2e;
-  if (!map_queries(&maps.q, a.q, p.d, p.G, p.Hkv, p.Tq, v.tpt)) return cudaErrorInvalidValue;
+  if (!map_queries(&maps.q, a.q, p.d, p.G, p.Hkv, p.Tq, v.box)) return cudaErrorInvalidValue;
   if (p.Tk > 0 && (!map_keys(&maps.k, a.k, p.d, p.Hkv, p.Tk) || !map_keys(&maps.v, a.v, p.d, p.Hkv, p.Tk)))
     return cudaErrorInvalidValue;
-  if (p.d == 128) return two ? launch_d<128, 2>(a, maps, v, s) : launch_d<128, 1>(a, maps, v, s);
-  return two ? launch_d<64, 2>(a, maps, v, s) : launch_d<64, 1>(a, maps, v, s);
+  if (p.d == 128)
+    return two   ? launch_d<128, 2, false>(a, maps, v, s)
+           : few ? launch_d<128, 1, true>(a, maps, v, s)
+                 : launch_d<128, 1, false>(a, maps, v, s);
+  return two   ? launch_d<64, 2, false>(a, maps, v, s)
+         : few ? launch_d<64, 1, true>(a, maps, v, s)
+               : launch_d<64, 1, false>(a, maps, v, s);
 }
 
 }  // namespace sla

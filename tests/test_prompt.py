@@ -16,7 +16,7 @@ class Plan(ctypes.Structure):
     """Mirror of the plan's header (csrc/prompt.cuh)."""
     _fields_ = [("status", ctypes.c_int), ("magic", ctypes.c_uint)] + \
         [(n, ctypes.c_int) for n in ("n_seq", "Hq", "Hkv", "G", "d", "causal")] + \
-        [("scale", ctypes.c_float), ("tiles", ctypes.c_int), ("Tq", ctypes.c_longlong), ("Tk", ctypes.c_longlong)] + \
+        [("scale", ctypes.c_float), ("tiles", ctypes.c_int), ("few", ctypes.c_int), ("Tq", ctypes.c_longlong), ("Tk", ctypes.c_longlong)] + \
         [(n, ctypes.c_int) for n in ("n_items", "n_joins", "n_slots", "join_rows", "n_keys", "n_kjoins", "n_kslots", "n_rows",
                                      "row_tiles")] + \
         [(n, ctypes.c_ulonglong) for n in ("items", "joins", "keys", "kjoins", "rows", "total")]
@@ -147,6 +147,8 @@ def test_serving_plans_list_no_backward(lib):
     (dict(d=96), "UNSUPPORTED"), (dict(Hq=129, Hkv=1), "UNSUPPORTED"), (dict(lens_q=[0, 0]), "INVALID_ARG"),
     (dict(softmax_scale=-1.0), "INVALID_ARG"), (dict(softmax_scale=float("nan")), "INVALID_ARG"),
     (dict(lens_q=[2 ** 30, 2 ** 30]), "UNSUPPORTED"), (dict(lens_k=[2 ** 31 - 1]), "UNSUPPORTED"),
+    (dict(lens_q=[2 ** 26], Hq=64, Hkv=64), "UNSUPPORTED"), (dict(lens_q=[1], lens_k=[2 ** 30], grad=True), "UNSUPPORTED"),
+    (dict(softmax_scale=1e-35), "INVALID_ARG"),
 ])
 def test_plan_refusals(lib, kw, code):
     a = dict(lens_q=[5], lens_k=None, Hq=4, Hkv=2, d=64, device="cpu")

@@ -30,6 +30,8 @@ CASES = [
     ([5], [0, ], 2, 1, 64, False),                   # no keys at all
     ([5, 4], [0, 3], 2, 1, 64, False),
     ([600], None, 2, 1, 128, True),
+    ([1300, 900], None, 2, 2, 128, True),
+    ([33, 1100], None, 4, 2, 64, False),
 ]
 IDS = lambda c: f"{c[0]}-{c[1]}-{c[2]}x{c[3]}-{c[4]}-{'causal' if c[5] else 'full'}".replace(" ", "")  # noqa: E731
 
@@ -236,6 +238,27 @@ def test_from_a_fresh_thread(cuda_lib):
         t.join()
     assert not any(isinstance(x, Exception) for x in got), got
     assert torch.equal(out, o) and all(torch.equal(a, b) for a, b in zip(dx, grads))
+
+
+def test_offsets_beyond_32_bits(cuda_lib):
+    """A cache of more than 2^31 values: its last sequence is read where it is."""
+    sla = cuda_lib
+    first, last = 2_100_000, 300
+    assert (first + last) * 8 * 128 > 2 ** 31
+    k, v = (torch.zeros(first + last, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    case = ([1, 3], [first, last], 16, 8, 128, True)
+    g = torch.Generator().manual_seed(14)
+    q = torch.randn(4, 16, 128, generator=g).bfloat16()
+    kl, vl = (torch.randn(last, 8, 128, generator=g).bfloat16() for _ in range(2))
+    k[first:], v[first:] = kl.cuda(), vl.cuda()
+    v[first - 1] = 3.0  # the first sequence: equal scores over zeros and one row of 3
+    plan = plan_of(sla, case)
+    o, lse = sla.prompt_forward(q.cuda(), k, v, plan)
+    ref = R.prompt(q[1:], kl, vl, [3], [last], True)
+    check_forward(case, o[1:], lse[1:], ref, q, kl)
+    # 3 / n for every value, from a sum of 2 million equal weights in float32
+    assert torch.allclose(o[0].float() * first, torch.full((16, 128), 3.0, device="cuda"), rtol=2.0 ** -7, atol=0)
+    assert torch.allclose(lse[0], torch.full((16,), math.log(first), device="cuda"), rtol=0, atol=1e-4)
 
 
 def test_refusals(cuda_lib):

@@ -274,6 +274,21 @@ def test_empty_and_refused(cuda_lib):
         sla.qk_norm_rope(x, x, w[:32], w, table)
 
 
+def test_offsets_beyond_32_bits(cuda_lib):
+    sla = cuda_lib
+    H, N, d = 40, 440_000, 128
+    assert H * N * d > 2 ** 31
+    x = torch.zeros(N, H, d, dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn(50, H, d, generator=torch.Generator().manual_seed(6)).bfloat16().cuda()
+    x[-50:] = tail
+    table = sla.rope_table(d)
+    y = sla.rope(x, table)
+    pos = torch.arange(N - 50, N, device="cuda")
+    assert torch.equal(y[-50:], sla.rope(tail, table, pos)) and (y[:-50] == 0).all()
+    hm = x.transpose(0, 1).unsqueeze(0)  # the same memory as [1, H, N, d]
+    assert torch.equal(sla.rope(hm, table)[0, :, -50:].transpose(0, 1), y[-50:])
+
+
 def test_streams_and_graphs(cuda_lib):
     sla = cuda_lib
     x = torch.randn(2, 3, 80, 128, device="cuda").bfloat16()
