@@ -457,7 +457,8 @@ sla_status sla_prompt_forward(const sla_rows* q, const sla_rows* k, const sla_ro
  * with backward = 1 (SLA_ERR_UNSUPPORTED otherwise).
  *   q, k, v, o, lse  the forward's inputs and results.
  *   rest             the forward's, or NULL: dO.O from the rounded O alone.
- *   dq, dk, dv       outputs; a key head's dk, dv add up its group's query heads.
+ *   dq, dk, dv       outputs, apart from every input; a key head's dk, dv add up its
+ *                    group's query heads.
  * Deterministic. Rows behind the last sequence are neither read nor written. */
 size_t sla_prompt_backward_workspace_size(const void* plan);
 sla_status sla_prompt_backward(const sla_rows* q, const sla_rows* k, const sla_rows* v, const sla_rows* o,

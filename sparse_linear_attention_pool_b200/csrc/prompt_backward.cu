@@ -47,6 +47,7 @@ constexpr int kSub = 128 * 128;  // 128 rows x 128 bytes (64 columns)
 // 16 bytes each. Bound: reading O and dO.
 template <int D>
 __global__ void __launch_bounds__(256) prompt_rowsum_kernel(const PromptGradDev a) {
+  asm volatile("griddepcontrol.launch_dependents;");  // the key kernel's first copies run beside this one
   constexpr int kLanes = D / 8;
   const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / kLanes;
   const int lane = threadIdx.x % kLanes;
@@ -159,10 +160,36 @@ __global__ void __launch_bounds__(320, 1)
   auto s_col = [&](int i) { return C::kTwoS && (i & 1) ? C::cS1 : C::cS; };
   auto phase = [&](int i) { return uint32_t(i / ST) & 1; };
 
-  if (threadIdx.x == 0) {
+  auto load_q = [&](int i) {
+    mbar_expect_tx(bar(qfull(i)), rows * D * 2);
+    for (int s = 0; s < D / 64; ++s)
+      tma_load_4d(sb + C::oQ + (i % ST) * C::kTileBytes + s * kSub, &maps.q, bar(qfull(i)), s * 64, 0,
+                  it.q0 + (it.t0 + i) * a.tpt, it.head);
+  };
+  auto load_g = [&](int i) {
+    mbar_expect_tx(bar(gfull(i)), rows * D * 2);
+    for (int s = 0; s < D / 64; ++s)
+      tma_load_4d(sb + C::oG + (i % ST) * C::kTileBytes + s * kSub, &maps.g, bar(gfull(i)), s * 64, 0,
+                  it.q0 + (it.t0 + i) * a.tpt, it.head);
+  };
+  if (warp == 8 && lane == 0) {
+    // the loader sets the barriers up and starts the first copies before the block meets
+    // (they are the caller's tensors: nothing here waits for the row sums yet)
     abort_sh = 0;
     for (int i = 0; i < kbQ + 5 * ST; ++i) mbar_init(bar(i), i == kbPr || i == kbDr ? 256 : i >= kbQ + 4 * ST ? 32 : 1);
     fence_barrier_init();
+    fence_async_smem();
+    if (n > 0) {
+      mbar_expect_tx(bar(kbKV), 2 * C::kTileBytes);
+      for (int s = 0; s < D / 64; ++s) {
+        tma_load_3d(sb + C::oK + s * kSub, &maps.k, bar(kbKV), s * 64, it.k0 + it.block * 128, it.head);
+        tma_load_3d(sb + C::oV + s * kSub, &maps.v, bar(kbKV), s * 64, it.k0 + it.block * 128, it.head);
+      }
+      for (int i = 0; i < min(n, ST); ++i) {
+        load_q(i);
+        load_g(i);
+      }
+    }
   }
   for (int x = threadIdx.x; x < (1 + 2 * ST) * (C::kStep / 16); x += 320) {
     const bool one = x < 128;  // 1.0 in bf16 is 0x3f80
@@ -185,14 +212,11 @@ __global__ void __launch_bounds__(320, 1)
   const uint32_t tb = tmem_base_sh;
 
   if (warp == 8) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the row sums are written
+    // from here on the row kernel may start where this one leaves SMs idle: it reads the row
+    // sums too, and nothing that this kernel writes
+    asm volatile("griddepcontrol.launch_dependents;");
     if (n > 0) {
-      if (lane == 0) {
-        mbar_expect_tx(bar(kbKV), 2 * C::kTileBytes);
-        for (int s = 0; s < D / 64; ++s) {
-          tma_load_3d(sb + C::oK + s * kSub, &maps.k, bar(kbKV), s * 64, it.k0 + it.block * 128, it.head);
-          tma_load_3d(sb + C::oV + s * kSub, &maps.v, bar(kbKV), s * 64, it.k0 + it.block * 128, it.head);
-        }
-      }
       const float2* ld = a.ld + it.head * (a.Tq * a.G);
       const float inv_c = 1.0f / a.scale_log2;
       // (lse2, D) of a tile, fetched a tile ahead: four rows per lane
@@ -208,16 +232,12 @@ __global__ void __launch_bounds__(320, 1)
         }
       };
       fetch(0);
-      int qi = 0, gi = 0;
+      int qi = min(n, ST), gi = qi;  // copies on their way
       for (int i = 0; i < n; ++i) {
-        const int tok = (it.t0 + i) * a.tpt;
         if (!wait_w(qempty(i), phase(i) ^ 1)) break;
-        if (lane == 0) {
+        if (lane == 0 && i >= ST) {
           qi = i + 1;
-          mbar_expect_tx(bar(qfull(i)), rows * D * 2);
-          for (int s = 0; s < D / 64; ++s)
-            tma_load_4d(sb + C::oQ + (i % ST) * C::kTileBytes + s * kSub, &maps.q, bar(qfull(i)), s * 64, 0,
-                        it.q0 + tok, it.head);
+          load_q(i);
         }
         __syncwarp();
         // the stage's -lse / scale and -D: its last readers, S and dP, came before the dK that freed the stage
@@ -233,12 +253,9 @@ __global__ void __launch_bounds__(320, 1)
         mbar_arrive(bar(lfull(i)));
         fetch(i + 1);
         if (!wait_w(gempty(i), phase(i) ^ 1)) break;
-        if (lane == 0) {
+        if (lane == 0 && i >= ST) {
           gi = i + 1;
-          mbar_expect_tx(bar(gfull(i)), rows * D * 2);
-          for (int s = 0; s < D / 64; ++s)
-            tma_load_4d(sb + C::oG + (i % ST) * C::kTileBytes + s * kSub, &maps.g, bar(gfull(i)), s * 64, 0,
-                        it.q0 + tok, it.head);
+          load_g(i);
         }
       }
       if (lane == 0) {
@@ -482,6 +499,7 @@ __global__ void __launch_bounds__(384, 1)
   if (it.q0 < 0 || it.nq < 1 || it.k0 < 0 || it.lk < 0 || it.q0 + (long long)it.nq > a.Tq ||
       it.k0 + (long long)it.lk > a.Tk || it.nq > a.row_tiles * a.tpt || it.head < 0) {
     if (threadIdx.x == 0) atomicExch(status, kDevBadIndex);
+    if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
   auto end_block = [&](int t) {
@@ -512,11 +530,39 @@ __global__ void __launch_bounds__(384, 1)
   auto kphase = [&](int s) { return uint32_t(s / KS) & 1; };
   auto vphase = [&](int s) { return uint32_t(s / VS) & 1; };
 
-  if (threadIdx.x == 0) {
+  auto load_k = [&](int s) {
+    mbar_expect_tx(bar(kfull(s)), C::kTileBytes);
+    for (int x = 0; x < D / 64; ++x)
+      tma_load_3d(sb + C::oK + (s % KS) * C::kTileBytes + x * kSub, &maps.k, bar(kfull(s)), x * 64,
+                  it.k0 + (n - 1 - s) * 128, it.head);
+  };
+  auto load_v = [&](int s) {
+    mbar_expect_tx(bar(vfull(s)), C::kTileBytes);
+    for (int x = 0; x < D / 64; ++x)
+      tma_load_3d(sb + C::oV + (s % VS) * C::kTileBytes + x * kSub, &maps.v, bar(vfull(s)), x * 64,
+                  it.k0 + (n - 1 - s) * 128, it.head);
+  };
+  if (warp == 8 && lane == 0) {  // the barriers and the first copies, before the block meets
     abort_sh = 0;
     for (int i = 0; i < rbKV + 2 * (KS + VS); ++i)
       mbar_init(bar(i), i == rbR0 || i == rbR1 || i == rbD0 || i == rbD1 ? 128 : 1);
     fence_barrier_init();
+    fence_async_smem();
+    const int rows = a.G * a.tpt;
+    for (int t = 0; t < 2; ++t) {
+      if ((t == 0 ? nb0 : nb1) == 0) continue;
+      mbar_expect_tx(bar(rbIn0 + t), 2 * rows * D * 2);
+      for (int s = 0; s < D / 64; ++s) {
+        tma_load_4d(sb + C::oQ + t * C::kTileBytes + s * kSub, &maps.q, bar(rbIn0 + t), s * 64, 0,
+                    it.q0 + t * a.tpt, it.head);
+        tma_load_4d(sb + C::oG + t * C::kTileBytes + s * kSub, &maps.g, bar(rbIn0 + t), s * 64, 0,
+                    it.q0 + t * a.tpt, it.head);
+      }
+    }
+    if (n > 0) {
+      load_k(0);
+      load_v(0);
+    }
   }
   if (warp == 9) tmem_alloc(smem_u32(&tmem_base_sh), 512);
   tc_fence_before();
@@ -530,30 +576,14 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 8) {
     reg_dec<40>();
     if (lane == 0 && n > 0) {
-      const int rows = a.G * a.tpt;
-      for (int t = 0; t < 2; ++t) {
-        if ((t == 0 ? nb0 : nb1) == 0) continue;
-        mbar_expect_tx(bar(rbIn0 + t), 2 * rows * D * 2);
-        for (int s = 0; s < D / 64; ++s) {
-          tma_load_4d(sb + C::oQ + t * C::kTileBytes + s * kSub, &maps.q, bar(rbIn0 + t), s * 64, 0,
-                      it.q0 + t * a.tpt, it.head);
-          tma_load_4d(sb + C::oG + t * C::kTileBytes + s * kSub, &maps.g, bar(rbIn0 + t), s * 64, 0,
-                      it.q0 + t * a.tpt, it.head);
-        }
-      }
-      int ks = 0, vs = 0;  // tiles on their way
-      for (int s = 0; s < n; ++s) {
-        const int row = it.k0 + (n - 1 - s) * 128;
+      int ks = 1, vs = 1;  // tiles on their way
+      for (int s = 1; s < n; ++s) {
         if (!wait(kempty(s), kphase(s) ^ 1)) break;
         ks = s + 1;
-        mbar_expect_tx(bar(kfull(s)), C::kTileBytes);
-        for (int x = 0; x < D / 64; ++x)
-          tma_load_3d(sb + C::oK + (s % KS) * C::kTileBytes + x * kSub, &maps.k, bar(kfull(s)), x * 64, row, it.head);
+        load_k(s);
         if (!wait(vempty(s), vphase(s) ^ 1)) break;
         vs = s + 1;
-        mbar_expect_tx(bar(vfull(s)), C::kTileBytes);
-        for (int x = 0; x < D / 64; ++x)
-          tma_load_3d(sb + C::oV + (s % VS) * C::kTileBytes + x * kSub, &maps.v, bar(vfull(s)), x * 64, row, it.head);
+        load_v(s);
       }
       if (nb0 > 0) wait_drain(rbIn0, 0);
       if (nb1 > 0) wait_drain(rbIn1, 0);
@@ -715,6 +745,9 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     tmem_dealloc(tb, 512);
   }
+  // This kernel may have started beside the key kernel and must not end before it: what
+  // follows in the stream reads both. One block's wait is the grid's.
+  if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 namespace {
@@ -733,9 +766,30 @@ cudaError_t launch_d(const PromptGradArgs& a, const PromptGradMaps& maps, const 
   const PromptPlan& p = *a.plan;
   const long long rows = p.Tq * p.Hq;
   prompt_rowsum_kernel<D><<<unsigned((rows * (D / 8) + 255) / 256), 256, 0, s>>>(v);
-  if (p.n_keys > 0) prompt_bwd_keys_kernel<D><<<p.n_keys, 320, KeyCfg<D>::kSmem, s>>>(maps, v);
+  // The key kernel starts beside the row sums and waits for them; the row kernel starts where
+  // the key kernel's last blocks leave SMs idle (the key kernel's blocks have all seen the row
+  // sums by then). Without key tiles the row kernel is an ordinary launch behind the row sums.
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = s;
+  cudaError_t e = cudaSuccess;
+  if (p.n_keys > 0) {
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(p.n_keys);
+    cfg.blockDim = dim3(320);
+    cfg.dynamicSmemBytes = KeyCfg<D>::kSmem;
+    e = cudaLaunchKernelEx(&cfg, prompt_bwd_keys_kernel<D>, maps, v);
+    if (e != cudaSuccess) return e;
+  }
+  cfg.gridDim = dim3(p.n_rows);
+  cfg.blockDim = dim3(384);
+  cfg.dynamicSmemBytes = RowCfg<D>::kSmem;
+  e = cudaLaunchKernelEx(&cfg, prompt_bwd_rows_kernel<D>, maps, v);
+  if (e != cudaSuccess) return e;
   if (p.n_kjoins > 0) prompt_keys_join_kernel<D><<<dim3(p.n_kjoins, 32, 2), 128, 0, s>>>(v);
-  prompt_bwd_rows_kernel<D><<<p.n_rows, 384, RowCfg<D>::kSmem, s>>>(maps, v);
   return cudaGetLastError();
 }
 

@@ -122,10 +122,42 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, FEW>::kThreads, FwdCfg<D, TIL
   };
   const uint32_t sb = smem_u32(smem);
 
-  if (threadIdx.x == 0) {
+  // ring positions, their barriers and their order: K0, K1, V0, K2, V1, ... - the next
+  // step's keys before this step's values
+  auto full = [&](int i) { return bKV + i % ST; };
+  auto empty = [&](int i) { return bKV + ST + i % ST; };
+  auto phase = [&](int i) { return uint32_t(i / ST) & 1; };
+  auto k_pos = [&](int s) { return s == 0 ? 0 : 2 * s - 1; };
+  auto v_pos = [&](int s) { return min(2 * s + 2, 2 * n - 1); };
+  auto load = [&](int i) {
+    const bool keys = i == 0 || ((i & 1) && i < 2 * n - 1);
+    const int b = bmax - 1 - (keys ? (i + 1) / 2 : i == 2 * n - 1 ? n - 1 : i / 2 - 1);
+    const CUtensorMap* m = keys ? &maps.k : &maps.v;
+    mbar_expect_tx(bar(full(i)), C::kTileBytes);
+    for (int s = 0; s < D / 64; ++s)
+      tma_load_3d(sb + C::oKV + (i % ST) * C::kTileBytes + s * C::kSub, m, bar(full(i)), s * 64, it.k0 + b * 128,
+                  it.head);
+  };
+  int issued = 0;
+  if (warp == C::kSoft && lane == 0) {
+    // the loader sets the barriers up and starts the first copies before the block meets
     abort_sh = 0;
     for (int i = 0; i < bKV + 2 * ST; ++i) mbar_init(bar(i), i >= bP0 && i <= bX1 ? 128 : 1);
     fence_barrier_init();
+    fence_async_smem();
+    const int rows = a.G * a.box;
+    for (int t = 0; t < TILES; ++t) {
+      if ((t == 0 ? nb0 : nb1) <= it.b0) continue;
+      mbar_expect_tx(bar(bQ0 + t), rows * D * 2);
+      for (int s = 0; s < D / 64; ++s)
+        tma_load_4d(sb + C::oQ + t * C::kTileBytes + s * C::kQSub, &maps.q, bar(bQ0 + t), s * 64, 0,
+                    it.q0 + t * a.tpt, it.head);
+      if (t == 0 || issued == 0) {  // the first keys right behind the first queries
+        load(0);
+        issued = 1;
+      }
+    }
+    for (; issued < min(2 * n, ST); ++issued) load(issued);
   }
   asm volatile("griddepcontrol.launch_dependents;");  // the join's launch runs behind this kernel
   if (warp == C::kSoft + 1) tmem_alloc(smem_u32(&tmem_base_sh), C::kCols);
@@ -133,37 +165,14 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, FEW>::kThreads, FwdCfg<D, TIL
   __syncthreads();
   tc_fence_after();
   const uint32_t tb = tmem_base_sh;
-  // the ring's order: K0, K1, V0, K2, V1, ... - the next step's keys before this step's values
-  auto k_pos = [&](int s) { return s == 0 ? 0 : 2 * s - 1; };
-  auto v_pos = [&](int s) { return min(2 * s + 2, 2 * n - 1); };
-  auto full = [&](int i) { return bKV + i % ST; };
-  auto empty = [&](int i) { return bKV + ST + i % ST; };
-  auto phase = [&](int i) { return uint32_t(i / ST) & 1; };
 
-  // A row's 128 scores stay in its thread's registers: the softmax warps take
-  // what the other four leave (2 x 232 + 40 = 3 x 168, the launch's own share).
   if (warp == C::kSoft) {
     if (TILES == 2) reg_dec<40>();
     if (lane == 0 && n > 0) {
-      const int rows = a.G * a.box;
-      for (int t = 0; t < TILES; ++t) {
-        if ((t == 0 ? nb0 : nb1) <= it.b0) continue;
-        mbar_expect_tx(bar(bQ0 + t), rows * D * 2);
-        for (int s = 0; s < D / 64; ++s)
-          tma_load_4d(sb + C::oQ + t * C::kTileBytes + s * C::kQSub, &maps.q, bar(bQ0 + t), s * 64, 0,
-                      it.q0 + t * a.tpt, it.head);
-      }
-      int issued = 0;
-      for (int i = 0; i < 2 * n; ++i) {
+      for (int i = issued; i < 2 * n; ++i) {
         if (!wait(empty(i), phase(i) ^ 1)) break;
         issued = i + 1;
-        const bool keys = i == 0 || ((i & 1) && i < 2 * n - 1);
-        const int b = bmax - 1 - (keys ? (i + 1) / 2 : i == 2 * n - 1 ? n - 1 : i / 2 - 1);
-        const CUtensorMap* m = keys ? &maps.k : &maps.v;
-        mbar_expect_tx(bar(full(i)), C::kTileBytes);
-        for (int s = 0; s < D / 64; ++s)
-          tma_load_3d(sb + C::oKV + (i % ST) * C::kTileBytes + s * C::kSub, m, bar(full(i)), s * 64,
-                      it.k0 + b * 128, it.head);
+        load(i);
       }
       // every copy has landed before the CTA can end
       if (nb0 > it.b0) wait_drain(bQ0, 0);
