@@ -18,8 +18,9 @@
 // V cos / sin pairs in registers and walks over the heads of its token, so the
 // sines are paid once per token and not per head.
 // The next heads' chunks are on their way meanwhile, as they came from memory.
-// V = 4: chunks of 8 as 16-byte loads held twice the registers, a third of the
-// warps and 3.9 TB/s. Neighbouring lane groups take neighbouring tokens: a
+// Chunks of 8 (16-byte loads) hold twice the registers and run half the warps:
+// 45.7 us against 35.3 (480p video queries), 570 against 481 (720p queries and keys).
+// Neighbouring lane groups take neighbouring tokens: a
 // head-major output is then written in runs of whole tiles.
 #include "sla_internal.cuh"
 
