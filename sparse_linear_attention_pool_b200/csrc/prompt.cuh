@@ -50,7 +50,8 @@ struct PromptPlan {
   int tiles;   // query tiles per forward item (1 or 2)
   int few;     // forward items have at most kPromptFew rows
   long long Tq, Tk;
-  int n_items, n_joins, n_slots, join_rows;  // join_rows: rows of a joined item up to its last live one
+  int n_items, n_joins, n_slots;
+  int join_rows, join_parts;  // most rows of a joined item (up to its last live one), most parts
   // backward (all 0 in a plan without it)
   int n_keys, n_kjoins, n_kslots, n_rows, row_tiles;  // n_rows: dQ items, of row_tiles query tiles each
   unsigned long long items, joins, keys, kjoins, rows, total;  // byte offsets

@@ -339,6 +339,7 @@ size_t layout(const sla_prompt_params& p, const Lists& L, PromptPlan* h) {
   h->n_slots = L.slots;
   for (const PromptJoin& j : L.joins) {
     const int tpt = kPromptTile / h->G;
+    h->join_parts = std::max(h->join_parts, j.n);
     h->join_rows = std::max(h->join_rows, j.nq > tpt ? kPromptTile + (j.nq - tpt) * h->G : j.nq * h->G);
   }
   h->n_keys = int(L.keys.size());

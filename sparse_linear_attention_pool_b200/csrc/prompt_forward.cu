@@ -448,30 +448,34 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, FEW>::kThreads, FwdCfg<D, TIL
 
 // Joins the partial results of rows whose keys were split: with L_i the parts'
 // log2-sums and M their maximum, O = sum 2^(L_i - M) O_i / sum 2^(L_i - M).
-// One warp per row, the parts in a fixed order: the lanes fetch 32 parts' L at once,
-// and every part's O row is one 16-byte (d = 128) or 8-byte load per lane.
-template <int D>
+// W warps per row (four rows, or one, per block): each finds the weights 2^(L_i - M)
+// and adds up every W-th part (a part's O row is one 16- or 8-byte load per lane); the
+// W sums are added in order. Bound: latency. Four warps where rows have many parts: a
+// single-token call over 100000 keys, 37 parts, takes 73 us, and 86 with one; one warp
+// where many rows have a few: a 1732-token batch, two parts, takes 17 us, and 23 with four.
+template <int D, int W>
 __global__ void __launch_bounds__(128) prompt_join_kernel(const PromptDev a) {
   constexpr int V = D / 32;
+  __shared__ float sum_sh[4][D], den_sh[4];
   const PromptJoin jn = a.joins[blockIdx.x];  // the plan's, written before the forward kernel began
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
-  const int lane = threadIdx.x & 31;
-  const int r = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y * (4 / W) + warp / W;
   const int t = r >> 7, rr = r & 127;
   const int tok = t * a.tpt + rr / a.G, g = rr - (rr / a.G) * a.G;
-  if (rr >= a.G * a.tpt || tok >= jn.nq || jn.q0 + (long long)tok >= a.Tq) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
+  if (rr >= a.G * a.tpt || tok >= jn.nq || jn.q0 + (long long)tok >= a.Tq) return;  // all W warps of the row
   const size_t rows = size_t(a.tiles) * 128;
+  const float* lse = a.part_lse + jn.first * rows + r;  // of part i: [i rows]
   float mx = -INFINITY;
-  for (int i = lane; i < jn.n; i += 32) mx = max_nan(mx, a.part_lse[(jn.first + i) * rows + r]);
+  for (int i = lane; i < jn.n; i += 32) mx = max_nan(mx, lse[i * rows]);
   for (int s = 16; s > 0; s >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, s));
   float o[V], den = 0.0f;
 #pragma unroll
   for (int x = 0; x < V; ++x) o[x] = 0.0f;
   for (int i0 = 0; i0 < jn.n && mx != -INFINITY; i0 += 32) {
-    const float w = i0 + lane < jn.n ? exp2f(a.part_lse[(jn.first + i0 + lane) * rows + r] - mx) : 0.0f;
+    const float w = i0 + lane < jn.n ? exp2f(lse[(i0 + lane) * rows] - mx) : 0.0f;
     const int end = min(32, jn.n - i0);
-#pragma unroll 4
-    for (int i = 0; i < end; ++i) {
+#pragma unroll 8
+    for (int i = warp % W; i < end; i += W) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
       const float* p = a.part + ((jn.first + i0 + i) * rows + r) * D + lane * V;
       float x[V];
@@ -482,6 +486,19 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const PromptDev a) {
       den += wi;
 #pragma unroll
       for (int y = 0; y < V; ++y) o[y] += wi * x[y];
+    }
+  }
+  if (W > 1) {  // one row per block: nobody has left
+#pragma unroll
+    for (int x = 0; x < V; ++x) sum_sh[warp][lane * V + x] = o[x];
+    if (lane == 0) den_sh[warp] = den;
+    __syncthreads();
+    if (warp > 0) return;
+    den = (den_sh[0] + den_sh[1]) + (den_sh[2] + den_sh[3]);
+#pragma unroll
+    for (int x = 0; x < V; ++x) {
+      const int c = lane * V + x;
+      o[x] = (sum_sh[0][c] + sum_sh[1][c]) + (sum_sh[2][c] + sum_sh[3][c]);
     }
   }
   const float inv = den == 0.0f ? 0.0f : 1.0f / den;
@@ -518,12 +535,14 @@ cudaError_t launch_d(const PromptArgs& a, const PromptMaps& maps, const PromptDe
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.plan->n_joins, (a.plan->join_rows + 3) / 4);
+  const bool many = a.plan->join_parts > 8;
+  cfg.gridDim = dim3(a.plan->n_joins, many ? a.plan->join_rows : (a.plan->join_rows + 3) / 4);
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prompt_join_kernel<D>, v);
+  return many ? cudaLaunchKernelEx(&cfg, prompt_join_kernel<D, 4>, v)
+              : cudaLaunchKernelEx(&cfg, prompt_join_kernel<D, 1>, v);
 }
 
 }  // namespace

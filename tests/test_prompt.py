@@ -17,7 +17,7 @@ class Plan(ctypes.Structure):
     _fields_ = [("status", ctypes.c_int), ("magic", ctypes.c_uint)] + \
         [(n, ctypes.c_int) for n in ("n_seq", "Hq", "Hkv", "G", "d", "causal")] + \
         [("scale", ctypes.c_float), ("tiles", ctypes.c_int), ("few", ctypes.c_int), ("Tq", ctypes.c_longlong), ("Tk", ctypes.c_longlong)] + \
-        [(n, ctypes.c_int) for n in ("n_items", "n_joins", "n_slots", "join_rows", "n_keys", "n_kjoins", "n_kslots", "n_rows",
+        [(n, ctypes.c_int) for n in ("n_items", "n_joins", "n_slots", "join_rows", "join_parts", "n_keys", "n_kjoins", "n_kslots", "n_rows",
                                      "row_tiles")] + \
         [(n, ctypes.c_ulonglong) for n in ("items", "joins", "keys", "kjoins", "rows", "total")]
 
