@@ -146,26 +146,40 @@ int chunk_for(const std::vector<int>& lengths, int most) {
 
 // Costs in units of one key block of a two-tile item, the only one on its SM.
 constexpr double kItemCost = 3.0;  // start, first loads and the store
+// The same for a two-tile item that the forward takes behind another one (measured, an item
+// more of 1 to 16 blocks on every SM: 0.9 steps at d = 64, 1.5 at d = 128).
+constexpr double kNextCost = 1.2;
 constexpr double kJoinCost = 3.0;  // the second launch
 // A step of a one-tile item, two of which share an SM, and of one that has its SM to
-// itself. At d = 128 the second copy of the keys costs bandwidth to shared memory
-// (18832 causal tokens, 2 heads: 200 us as one-tile items, 174 as two-tile ones); at
-// d = 64 the exponentials bound both (16384 tokens, 16 heads: 669 and 643 us; 8192 full
-// ones, whose two-tile items leave half of their last round idle: 349 and 418).
-double one_tile_step(int d, bool shared) { return shared ? (d == 128 ? 1.4 : 0.97) : (d == 128 ? 0.9 : 0.7); }
+// itself. At d = 128 the second copy of the keys costs bandwidth to shared memory (4096
+// causal tokens, 16 heads: 82 us as one-tile items, 58 as two-tile ones). At d = 64 the
+// exponentials bound both, and the items' ends decide (8192 causal tokens, 16 heads: 186
+// and 177 us; 4096: 61 and 53), or the last round (8192 full ones, whose two-tile items
+// leave half of it idle, while the last one-tile items have an SM each: 356 and 414).
+double one_tile_step(int d, bool shared) { return shared ? (d == 128 ? 1.4 : 1.02) : (d == 128 ? 0.9 : 0.7); }
 
 // full_rows: how full of live rows the tiles are
-double split_cost(const std::vector<PromptItem>& items, int chunk, int tiles, double full_rows, int d) {
+// again: a CTA of two tiles takes item after item
+double split_cost(const std::vector<PromptItem>& items, int chunk, int tiles, double full_rows, int d, bool again) {
   std::vector<double> cost;
   size_t parts = 0;
   for (const PromptItem& it : items) parts += pieces(it.b1, chunk);
   const bool shared = tiles == 1 && parts > size_t(kPromptSms);
-  const double step = tiles == 2 ? 1.0 : one_tile_step(d, shared);
   double joins = 0.0;  // rows of partial results, in tiles: written and read once more in float32
   for (const PromptItem& it : items) {
     const int n = pieces(it.b1, chunk);
     if (n > 1) joins += n * tiles;
-    for (int i = 0; i < n; ++i) cost.push_back(kItemCost + step * ((it.b1 + n - 1) / n));
+    for (int i = 0; i < n; ++i) cost.push_back((it.b1 + n - 1) / n);
+  }
+  // the longest first, as they are handed out
+  std::sort(cost.begin(), cost.end(), std::greater<double>());
+  // one-tile items: of the last round's, those that share their SM
+  const size_t left = cost.size() % (2 * kPromptSms);
+  const double paired = left <= size_t(kPromptSms) ? 0.0 : 2.0 * (left - kPromptSms) / left;
+  const double both = one_tile_step(d, true), last = paired * both + (1.0 - paired) * one_tile_step(d, false);
+  for (size_t i = 0; i < cost.size(); ++i) {
+    const double step = tiles == 2 ? 1.0 : i < cost.size() - left ? both : last;
+    cost[i] = (again && tiles == 2 && i >= size_t(kPromptSms) ? kNextCost : kItemCost) + step * cost[i];
   }
   return makespan(cost, shared ? 2 * kPromptSms : kPromptSms) + (joins > 0.0 ? kJoinCost + full_rows * joins / kPromptSms : 0.0);
 }
@@ -197,7 +211,7 @@ Lists make_lists(const sla_prompt_params& p) {
       for (int rounds = 1; rounds <= 3; ++rounds) chunks.push_back(chunk_for(lengths, rounds * kPromptSms * (3 - tiles)));
     }
     for (int chunk : chunks) {
-      const double c = split_cost(items, chunk, tiles, std::min(1.0, double(longest) / tpt), p.d);
+      const double c = split_cost(items, chunk, tiles, std::min(1.0, double(longest) / tpt), p.d, true);
       if (base.empty() || c < best) {
         best = c;
         best_chunk = chunk;
@@ -241,7 +255,7 @@ void add_backward(const sla_prompt_params& p, Lists& L) {
       L.row_tiles = 2;
       break;
     }
-    const double c = split_cost(rows, 0, 2, 1.0, p.d) * (tiles == 2 ? 1.0 : 0.8);  // one CTA per SM either way
+    const double c = split_cost(rows, 0, 2, 1.0, p.d, false) * (tiles == 2 ? 1.0 : 0.8);  // one CTA per SM either way
     if (tiles == 2 || c < best) {
       best = c;
       L.rows = std::move(rows);

@@ -234,12 +234,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, FEW>::kThreads, FwdCfg<D, TIL
         auto ask = [&]() {
           if (!C::kAgain) return;
           if (job > 0) fence_async_smem();
-          mbar_expect_tx(bar(bNext), 16);
-          asm volatile(
-              "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                  smem_u32(&next_sh)),
-              "r"(bar(bNext))
-              : "memory");
+          ask_block(&next_sh, bar(bNext));
         };
         bool asked = false, ok = true;
         for (int t = 0; t < TILES; ++t) {
@@ -264,23 +259,14 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, FEW>::kThreads, FwdCfg<D, TIL
         if (!asked) ask();
         if (!C::kAgain) break;
         // the answer, and the item, for everyone
-        uint32_t block = 0, have = 0;
         if (!wait_drain(bNext, job & 1)) break;
-        asm volatile(
-            "{\n .reg .pred p;\n .reg .b128 h;\n .reg .b32 y, z, u;\n ld.shared.b128 h, [%2];\n"
-            " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
-            " selp.u32 %1, 1, 0, p;\n mov.u32 %0, 0;\n"
-            " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, u}, h;\n}\n"
-            : "=r"(block), "=r"(have)
-            : "r"(smem_u32(&next_sh))
-            : "memory");
+        const int block = answered_block(&next_sh);
         PromptItem it{};
-        if (have && ok) it = a.items[block];
-        if (have && ok && !sound(it)) {
+        if (block >= 0 && ok) it = a.items[block];
+        if (it.nq != 0 && !sound(it)) {
           atomicExch(status, kDevBadIndex);
           it.nq = 0;
         }
-        if (!have) it.nq = 0;
         if (job > 1 && !wait(bJobE0 + (job & 1), ((job >> 1) - 1) & 1)) break;
         job_sh[job & 1] = it;
         mbar_arrive(bar(bJobF0 + (job & 1)));

@@ -120,6 +120,30 @@ __device__ __forceinline__ void ex2_fma(uint64_t x2, float& lo, float& hi) {
   hi = __int_as_float(__float_as_int(b) + (__float_as_int(j) << 23));
 }
 
+// Taking over a block of the grid that has not started (one thread asks; blocks are handed
+// out in order). The answer arrives in `next`, 16 bytes in shared memory, on the barrier;
+// after an answer without a block none may be asked for again.
+__device__ __forceinline__ void ask_block(uint4* next, uint32_t bar) {
+  mbar_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(next)),
+      "r"(bar)
+      : "memory");
+}
+// Its index, or -1.
+__device__ __forceinline__ int answered_block(uint4* next) {
+  uint32_t block, have;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 h;\n .reg .b32 y, z, u;\n ld.shared.b128 h, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n selp.u32 %1, 1, 0, p;\n mov.u32 %0, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, u}, h;\n}\n"
+      : "=r"(block), "=r"(have)
+      : "r"(smem_u32(next))
+      : "memory");
+  return have ? int(block) : -1;
+}
+
 // ---- host: tensor maps of packed tokens ----
 // Packed query rows: (d, G, tokens, key heads), boxes of 64 values x G heads x tpt tokens.
 inline bool map_queries(CUtensorMap* m, const PromptTensor& t, int d, int G, int Hkv, long long T, int tpt) {
