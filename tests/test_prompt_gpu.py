@@ -107,6 +107,27 @@ def test_growing_maxima(cuda_lib):
     check_forward(case, o, lse, R.prompt(q, k, v, lq, lk, False), q, k)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d", [64, 128])
+def test_more_items_than_sms(cuda_lib, d, causal):
+    """Over a thousand items of two tiles, so that every SM takes several: second tiles that are not there,
+    items without keys, rows that see nothing, last blocks of every length; another sequence's NaN."""
+    sla = cuda_lib
+    lens = [129, 1, 64, 200, 300, 5, 128, 63] * 13, [129, 40, 0, 500, 100, 260, 128, 63] * 13
+    case = (*lens, 16, 8, d, causal)
+    q, k, v, _, lq, lk = make(case, seed=5)
+    plan = plan_of(sla, case)
+    o, lse = sla.prompt_forward(q.cuda(), k.cuda(), v.cuda(), plan)
+    assert sla.read_device_status(plan.device_bytes) == 0
+    check_forward(case, o, lse, R.prompt(q, k, v, lq, lk, causal), q, k)
+    bad, first = 51, (sum(lq[:51]), sum(lk[:51]))  # 500 keys
+    k[first[1]:first[1] + lk[bad]], v[first[1]:first[1] + lk[bad]] = math.nan, math.inf
+    p = sla.prompt_attention(q.cuda(), k.cuda(), v.cuda(), plan)
+    rest = torch.ones(sum(lq), dtype=torch.bool)
+    rest[first[0]:first[0] + lq[bad]] = False
+    assert torch.equal(p.cpu()[rest], o.cpu()[rest]) and p.cpu()[~rest].isnan().all()
+
+
 def test_strided_rows_and_rows_behind_the_last_sequence(cuda_lib):
     sla = cuda_lib
     case = ([70, 200, 33], None, 4, 2, 64, True)
