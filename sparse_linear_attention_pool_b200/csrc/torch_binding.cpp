@@ -149,6 +149,7 @@ struct RopeMeta : torch::CustomClassHolder {
   int64_t N = 0;
   OptInt rows;
   bool inverse = false;
+  bool zero_behind = false;  // rows behind N of the result are zero: it is a gradient
   float eps = 0.0f;
   std::vector<int64_t> sizes;
 };
@@ -161,7 +162,9 @@ struct RopeFunction : torch::autograd::Function<RopeFunction> {
   static Tensor forward(AutogradContext* ctx, const Tensor& x, RopeMetaPtr meta) {
     ctx->saved_data["meta"] = c10::IValue::make_capsule(meta);
     if (meta->pos.defined()) ctx->save_for_backward({meta->pos});
-    return run_rope(x, *meta->table, meta->pos, meta->N, out_for(x, {}, meta->rows, meta->N), meta->inverse);
+    const Tensor y = run_rope(x, *meta->table, meta->pos, meta->N, out_for(x, {}, meta->rows, meta->N), meta->inverse);
+    if (meta->zero_behind) zero_tail(y, meta->N);
+    return y;
   }
   static variable_list backward(AutogradContext* ctx, variable_list grads) {
     const auto meta = rope_meta(ctx);
@@ -172,6 +175,7 @@ struct RopeFunction : torch::autograd::Function<RopeFunction> {
       back->pos = pos;
       back->N = meta->N;
       back->inverse = !meta->inverse;
+      back->zero_behind = true;
       back->sizes = meta->sizes;
       TORCH_CHECK(!meta->rows, "rope with rows is not differentiable twice");
       return {apply(dy, back), Tensor()};
