@@ -33,6 +33,17 @@ void check_status(sla_status st, const char* call) {
 
 void* stream_of(const Tensor& x) { return c10::cuda::getCurrentCUDAStream(x.device().index()).stream(); }
 
+// A plan and a table keep memory between calls, allocated on the stream that was current when they
+// were made (`home`). A call on another stream tells the allocator: dropped right after the call,
+// the memory is not handed out again before that stream is done with it.
+cudaStream_t home_of(const Tensor& kept) {
+  return kept.is_cuda() ? c10::cuda::getCurrentCUDAStream(kept.device().index()).stream() : nullptr;
+}
+void record_use(const Tensor& kept, cudaStream_t home) {
+  const auto now = c10::cuda::getCurrentCUDAStream(kept.device().index());
+  if (now.stream() != home) kept.record_stream(now);
+}
+
 // ---------------------------------------------------------------------------
 // rotary positions
 // ---------------------------------------------------------------------------
@@ -42,6 +53,7 @@ struct RopeTable {
   OptTensor axis;
   float gain;
   int rot_dim, layout, n_axes;
+  cudaStream_t home;
 };
 using TablePtr = std::shared_ptr<RopeTable>;
 
@@ -84,6 +96,8 @@ int64_t count_of(const Tensor& x, const OptInt& N) {
 // The rotation of a call, positions checked against B and N; `pos` may be undefined.
 sla_rope_spec spec_of(const RopeTable& t, const Tensor& pos, int64_t B, int64_t N, const at::Device& device) {
   TORCH_CHECK_VALUE(t.turns.device() == device, "the table is on another device");
+  record_use(t.turns, t.home);
+  if (t.axis) record_use(*t.axis, t.home);
   sla_rope_spec s{};
   s.turns = static_cast<const unsigned long long*>(t.turns.data_ptr());
   s.axis = t.axis ? static_cast<const unsigned char*>(t.axis->data_ptr()) : nullptr;
@@ -363,6 +377,7 @@ struct PromptPlan {
   std::vector<unsigned long long> host;  // 8-byte aligned
   size_t bytes;
   Tensor device;
+  cudaStream_t home;
   int64_t Tq, Tk, Hq, Hkv, d;
   bool grad;
   int64_t forward_workspace, backward_workspace;
@@ -398,6 +413,7 @@ std::tuple<Tensor, Tensor, Tensor> run_forward(Tensor q, Tensor k, Tensor v, con
   const sla_rows rq = rows_of(q, p.Tq, p.Hq, p, "q"), rk = rows_of(k, p.Tk, p.Hkv, p, "k"),
                  rv = rows_of(v, p.Tk, p.Hkv, p, "v");
   const sla_rows ro = out_rows(out, q, p.Tq, p.Hq, p, "out");
+  record_use(p.device, p.home);
   Tensor lse, rest, ws;
   if (want_rest) rest = at::empty({p.Tq, p.Hq, p.d}, q.options());
   if (want_lse) lse = at::empty({p.Tq, p.Hq}, q.options().dtype(at::kFloat));
@@ -431,6 +447,7 @@ std::tuple<Tensor, Tensor, Tensor> run_backward(Tensor q, Tensor k, Tensor v, Te
                           rest.size(0) == p.Tq && rest.size(1) == p.Hq && rest.size(2) == p.d &&
                           rest.device() == p.device.device(),
                       "rest: prompt_forward's [", p.Tq, ", ", p.Hq, ", ", p.d, "] bfloat16");
+  record_use(p.device, p.home);
   const bool fresh = !dq.defined();
   const sla_rows oq = out_rows(dq, q, p.Tq, p.Hq, p, "dq"), ok = out_rows(dk, k, p.Tk, p.Hkv, p, "dk"),
                  ov = out_rows(dv, v, p.Tk, p.Hkv, p, "dv");
@@ -514,7 +531,7 @@ PYBIND11_MODULE(_sla_torch, m) {
   });
   py::class_<RopeTable, TablePtr>(m, "RopeTable")
       .def(py::init([](Tensor turns, OptTensor axis, double gain, int rot_dim, int layout, int n_axes) {
-        return std::make_shared<RopeTable>(RopeTable{turns, axis, float(gain), rot_dim, layout, n_axes});
+        return std::make_shared<RopeTable>(RopeTable{turns, axis, float(gain), rot_dim, layout, n_axes, home_of(turns)});
       }));
   py::class_<PromptPlan, PlanPtr>(m, "PromptPlan")
       .def(py::init([](py::bytes host, Tensor device, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t d,
@@ -525,6 +542,7 @@ PYBIND11_MODULE(_sla_torch, m) {
         std::memcpy(p->host.data(), raw.data(), raw.size());
         p->bytes = raw.size();
         p->device = device;
+        p->home = home_of(device);
         p->Tq = Tq;
         p->Tk = Tk;
         p->Hq = Hq;

@@ -83,7 +83,7 @@ def prompt_forward(q, k, v, plan: PromptPlan, *, out=None, want_lse: bool = True
     backward's gradients a little more exact. Rows of O behind the plan's last token are not written."""
     args = (q, k, v, plan._c, out, want_lse, want_rest, workspace)
     if stream is not None:
-        with on_stream(stream, q.device):
+        with on_stream(stream, q.device, *args):
             made = _sla.prompt_forward(*args)
     else:
         made = _sla.prompt_forward(*args)
@@ -96,7 +96,7 @@ def prompt_backward(q, k, v, o, lse, do, plan: PromptPlan, *, rest=None, out=Non
     last token are zero, or with `out` as they were."""
     args = (q, k, v, o, lse, rest, do, plan._c, out, workspace)
     if stream is not None:
-        with on_stream(stream, q.device):
+        with on_stream(stream, q.device, *args):
             return _sla.prompt_backward(*args)
     return _sla.prompt_backward(*args)
 
@@ -105,6 +105,6 @@ def prompt_attention(q, k, v, plan: PromptPlan, *, stream=None):
     """O = softmax(scale Q K^T + mask) V for the plan's packed sequences, [rows of q, Hq, d].
     Differentiable in q, k and v (with a plan made for it)."""
     if stream is not None:
-        with on_stream(stream, q.device):
+        with on_stream(stream, q.device, q, k, v):
             return _sla.prompt_attention(q, k, v, plan._c)
     return _sla.prompt_attention(q, k, v, plan._c)

@@ -116,10 +116,16 @@ def rope_table(rot_dim: int, *, layout: str = "interleaved", freqs: Optional[Seq
                      tuple(made))
 
 
-def on_stream(stream, device):
-    """A context in which `stream` (a torch stream or an integer handle) is the current one."""
+def on_stream(stream, device, *used):
+    """A context in which `stream` (a torch stream or an integer handle) is the current one. The
+    memory of the tensors `used` is not handed out again before that stream is done with it."""
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
+    for t in used:
+        if isinstance(t, (tuple, list)):
+            on_stream(stream, device, *t)
+        elif isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
     return torch.cuda.stream(stream)
 
 
@@ -133,7 +139,7 @@ def rope(x, table: RopeTable, positions=None, *, N: Optional[int] = None, rows: 
     behind N are not written. out: a tensor to write to (x itself is allowed).
     inverse rotates back by the same angles."""
     if stream is not None:
-        with on_stream(stream, x.device):
+        with on_stream(stream, x.device, x, positions, out):
             return _sla.rope(x, table._c, positions, N, rows, out, inverse)
     return _sla.rope(x, table._c, positions, N, rows, out, inverse)
 
@@ -148,7 +154,7 @@ def qk_norm_rope(q, k, wq, wk, table: Optional[RopeTable] = None, positions=None
     out: a pair of tensors."""
     t = None if table is None else table._c
     if stream is not None:
-        with on_stream(stream, q.device):
+        with on_stream(stream, q.device, q, k, wq, wk, positions, out):
             return _sla.qk_norm_rope(q, k, wq, wk, t, positions, eps, N, rows, out)
     return _sla.qk_norm_rope(q, k, wq, wk, t, positions, eps, N, rows, out)
 
@@ -162,6 +168,6 @@ def qk_norm_rope_backward(q, k, wq, wk, dyq, dyk, table: Optional[RopeTable] = N
     t = None if table is None else table._c
     args = (q, k, wq, wk, dyq, dyk, t, positions, eps, N, want_weight_grad, workspace)
     if stream is not None:
-        with on_stream(stream, q.device):
+        with on_stream(stream, q.device, *args):
             return _sla.qk_norm_rope_backward(*args)
     return _sla.qk_norm_rope_backward(*args)

@@ -42,3 +42,72 @@ def test_rope_gradient_rows_behind_N_with_a_graph(cuda_lib, packed, inverse):
     assert (ddy[tail] == 0).all()
     assert torch.equal(ddy.narrow(0 if packed else 2, 0, N),
                        sla.rope(v.detach(), table, N=N, inverse=inverse).narrow(0 if packed else 2, 0, N))
+
+
+def test_memory_outlives_a_call_on_another_stream(cuda_lib):
+    """Dropped right after a call on another stream, a plan, a table and the tensors given with
+    `stream` keep their memory until that stream is done."""
+    sla = cuda_lib
+    side = torch.cuda.Stream()
+    x = randn(6, 2, 64, seed=1)
+    w = torch.ones(64, device="cuda", dtype=torch.bfloat16)
+    grid = torch.arange(6, device="cuda").repeat(2, 1)
+    made = lambda: sla.prompt_plan([6], Hq=2, Hkv=2, d=64)  # noqa: E731
+    o, lse = sla.prompt_forward(x, x, x, made())
+
+    def plan_in(f):
+        p = made()
+        kept = [p.device_bytes]
+        f(p)
+        return kept
+
+    def table_in(f):
+        t = sla.rope_table(64, sections=(16, 16))
+        kept = [t.turns, t.axis]
+        f(t)
+        return kept
+
+    def tensors(f, *ts):
+        ts = [t.clone() for t in ts]
+        f(*ts)
+        return ts
+
+    def on_side(f):
+        with torch.cuda.stream(side):
+            return f()
+
+    def trained(p):
+        leaf = x.clone().requires_grad_(True)
+        on_side(lambda: sla.prompt_attention(leaf, x, x, p).float().sum().backward())
+
+    table, plan = sla.rope_table(64), made()
+    calls = [
+        lambda: plan_in(lambda p: sla.prompt_forward(x, x, x, p, stream=side)),
+        lambda: plan_in(lambda p: sla.prompt_attention(x, x, x, p, stream=side.cuda_stream)),
+        lambda: plan_in(lambda p: on_side(lambda: sla.prompt_attention(x, x, x, p))),
+        lambda: plan_in(lambda p: sla.prompt_backward(x, x, x, o, lse, x, p, stream=side)),
+        lambda: plan_in(trained),
+        lambda: table_in(lambda t: sla.rope(x, t, grid, stream=side)),
+        lambda: table_in(lambda t: on_side(lambda: sla.rope(x, t, grid))),
+        lambda: table_in(lambda t: sla.qk_norm_rope(x, x, w, w, t, grid, stream=side)),
+        lambda: table_in(lambda t: sla.qk_norm_rope_backward(x, x, w, w, x, x, t, grid, stream=side)),
+        lambda: tensors(lambda a, p, y: sla.rope(a, table, p, out=y, stream=side), x, grid[0].contiguous(), x),
+        lambda: tensors(lambda a, b, u, v, y, z: sla.qk_norm_rope(a, b, u, v, table, out=(y, z), stream=side), x, x, w, w, x, x),
+        lambda: tensors(lambda a, b, c, y: sla.prompt_forward(a, b, c, plan, out=y, stream=side), x, x, x, x),
+        lambda: tensors(lambda a, b, c: sla.prompt_attention(a, b, c, plan, stream=side), x, x, x),
+        lambda: tensors(lambda a, b, c, s: sla.prompt_backward(x, x, x, a, s, b, plan, out=(c, x.clone(), x.clone()), stream=side),
+                        o, x, x, lse),
+    ]
+    for i, call in enumerate(calls):
+        call()  # what a first call sets up
+        torch.cuda.synchronize()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(400_000_000)  # clocks: a fifth of a second
+        kept = call()
+        sizes = [(t.shape, t.dtype, t.data_ptr()) for t in kept]
+        del kept
+        again = [torch.empty(s, dtype=d, device="cuda") for s, d, _ in sizes for _ in range(64)]
+        assert not side.query(), i  # else nothing was tested
+        assert not {p for *_, p in sizes} & {t.data_ptr() for t in again}, i
+        torch.cuda.synchronize()
