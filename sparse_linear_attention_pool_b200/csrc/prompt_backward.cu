@@ -32,7 +32,7 @@ struct PromptGradDev {
   const __nv_bfloat16* rest;
   float2* ld;
   float* part;
-  int Hq, Hkv, G, tpt, causal, row_tiles;
+  int Hq, Hkv, G, tpt, causal, row_tiles, n_kslots;
   long long Tq, Tk;
   float scale, scale_log2;
 };
@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(320, 1)
   int* status = reinterpret_cast<int*>(a.plan_dev);
   const PromptKeys it = a.keys[blockIdx.x];
   if (it.k0 < 0 || it.lk < 1 || it.q0 < 0 || it.lq < 0 || it.k0 + (long long)it.lk > a.Tk ||
-      it.q0 + (long long)it.lq > a.Tq || it.block < 0 || it.block * 128LL >= it.lk || it.head < 0 || it.t0 < 0) {
+      it.q0 + (long long)it.lq > a.Tq || it.block < 0 || it.block * 128LL >= it.lk || it.head < 0 ||
+      it.head >= a.Hkv || it.slot >= a.n_kslots || it.t0 < 0 || (it.t1 > it.t0 && (it.t1 - 1LL) * a.tpt >= it.lq)) {
     if (threadIdx.x == 0) atomicExch(status, kDevBadIndex);
     return;
   }
@@ -446,6 +447,11 @@ template <int D>
 __global__ void __launch_bounds__(128) prompt_keys_join_kernel(const PromptGradDev a) {
   const PromptKeysJoin jn = a.kjoins[blockIdx.x];
   const int lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5), which = blockIdx.z;
+  if (jn.row < 0 || jn.row + (long long)jn.nk > a.Tk || jn.head < 0 || jn.head >= a.Hkv || jn.first < 0 || jn.n < 0 ||
+      jn.first + (long long)jn.n > a.n_kslots) {
+    if (threadIdx.x == 0) atomicExch(reinterpret_cast<int*>(a.plan_dev), kDevBadIndex);
+    return;
+  }
   if (r >= jn.nk) return;
   float x[D / 32];
 #pragma unroll
@@ -503,7 +509,8 @@ __global__ void __launch_bounds__(384, 1)
   int* status = reinterpret_cast<int*>(a.plan_dev);
   const PromptItem it = a.rows[blockIdx.x];
   if (it.q0 < 0 || it.nq < 1 || it.k0 < 0 || it.lk < 0 || it.q0 + (long long)it.nq > a.Tq ||
-      it.k0 + (long long)it.lk > a.Tk || it.nq > a.row_tiles * a.tpt || it.head < 0) {
+      it.k0 + (long long)it.lk > a.Tk || it.nq > a.row_tiles * a.tpt || it.head < 0 ||
+      it.head >= a.Hkv) {
     if (threadIdx.x == 0) atomicExch(status, kDevBadIndex);
     if (blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
@@ -829,6 +836,7 @@ cudaError_t launch_prompt_backward(const PromptGradArgs& a, cudaStream_t s) {
   v.tpt = kPromptTile / p.G;
   v.causal = p.causal;
   v.row_tiles = p.row_tiles;
+  v.n_kslots = p.n_kslots;
   v.Tq = p.Tq;
   v.Tk = p.Tk;
   v.scale = p.scale;

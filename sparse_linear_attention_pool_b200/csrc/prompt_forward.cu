@@ -46,9 +46,10 @@ struct PromptDev {
   long long o_row, o_head;
   __nv_bfloat16* rest;
   float *lse, *part, *part_lse;
-  int Hq, G, tpt, box, causal, tiles;  // box: tokens that a copy of Q brings
+  int Hq, Hkv, G, tpt, box, causal, tiles;  // box: tokens that a copy of Q brings
+  int n_slots;
   long long Tq, Tk;
-  float scale, scale_log2;
+  float scale_log2;
 };
 
 namespace {
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, FEW>::kThreads, FwdCfg<D, TIL
   auto sound = [&](const PromptItem& it) {
     return it.q0 >= 0 && it.nq >= 1 && it.k0 >= 0 && it.lk >= 0 && it.q0 + (long long)it.nq <= a.Tq &&
            it.k0 + (long long)it.lk <= a.Tk && it.nq <= TILES * a.tpt && (!FEW || it.nq <= a.box) && it.b0 >= 0 &&
-           it.head >= 0;
+           it.head >= 0 && it.head < a.Hkv && it.slot < a.n_slots;
   };
   auto work_of = [&](const PromptItem& it) {
     auto end_block = [&](int t) {
@@ -262,10 +263,12 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, FEW>::kThreads, FwdCfg<D, TIL
         if (!wait_drain(bNext, job & 1)) break;
         const int block = answered_block(&next_sh);
         PromptItem it{};
-        if (block >= 0 && ok) it = a.items[block];
-        if (it.nq != 0 && !sound(it)) {
-          atomicExch(status, kDevBadIndex);
-          it.nq = 0;
+        if (block >= 0 && ok) {
+          it = a.items[block];
+          if (!sound(it)) {
+            atomicExch(status, kDevBadIndex);
+            it.nq = 0;
+          }
         }
         if (job > 1 && !wait(bJobE0 + (job & 1), ((job >> 1) - 1) & 1)) break;
         job_sh[job & 1] = it;
@@ -594,6 +597,10 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const PromptDev a) {
   const int t = r >> 7, rr = r & 127;
   const int tok = t * a.tpt + rr / a.G, g = rr - (rr / a.G) * a.G;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
+  if (jn.q0 < 0 || jn.head < 0 || jn.head >= a.Hkv || jn.first < 0 || jn.n < 0 || jn.first + (long long)jn.n > a.n_slots) {
+    if (threadIdx.x == 0) atomicExch(reinterpret_cast<int*>(a.plan_dev), kDevBadIndex);
+    return;
+  }
   if (rr >= a.G * a.tpt || tok >= jn.nq || jn.q0 + (long long)tok >= a.Tq) return;  // all W warps of the row
   const size_t rows = size_t(a.tiles) * 128;
   const float* lse = a.part_lse + jn.first * rows + r;  // of part i: [i rows]
@@ -700,6 +707,8 @@ cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s) {
   v.part = a.part;
   v.part_lse = a.part_lse;
   v.Hq = p.Hq;
+  v.Hkv = p.Hkv;
+  v.n_slots = p.n_slots;
   v.G = p.G;
   v.tpt = kPromptTile / p.G;
   v.box = p.few ? kPromptFew / p.G : v.tpt;
@@ -707,7 +716,6 @@ cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s) {
   v.tiles = p.tiles;
   v.Tq = p.Tq;
   v.Tk = p.Tk;
-  v.scale = p.scale;
   v.scale_log2 = p.scale * kLog2e;
   if (!map_queries(&maps.q, a.q, p.d, p.G, p.Hkv, p.Tq, v.box)) return cudaErrorInvalidValue;
   if (p.Tk > 0 && (!map_keys(&maps.k, a.k, p.d, p.Hkv, p.Tk) || !map_keys(&maps.v, a.v, p.d, p.Hkv, p.Tk)))

@@ -430,3 +430,99 @@ def test_backward_graph_and_shared_leaves(cuda_lib):
     serve = sla.prompt_plan([3], [40], Hq=4, Hkv=2, d=128)
     with pytest.raises(ValueError):
         sla.prompt_attention(q[:3].clone().requires_grad_(True), k[:40], v[:40], serve)
+
+
+def broken(plan, table, index, **fields):
+    """The plan's device copy with some words of one of its items changed."""
+    from tests import test_prompt as T
+
+    h = T.read(plan)[0]
+    names = dict(items=T.ITEM, rows=T.ITEM, joins=T.JOIN, keys=T.KEYS, kjoins=T.KJOIN)[table]
+    words = plan.device_bytes.view(torch.int32)
+    for name, value in fields.items():
+        words[getattr(h, table) // 4 + index * len(names) + names.index(name)] = value
+    return h
+
+
+FORWARD_FAULTS = [("items", dict(head=2)), ("items", dict(head=-1)), ("items", dict(slot=0)), ("items", dict(nq=0)),
+                  ("items", dict(q0=300)), ("items", dict(lk=1000))]
+
+
+@pytest.mark.parametrize("table,fields", FORWARD_FAULTS, ids=str)
+@pytest.mark.parametrize("lens,d", [([300], 64), ([129] * 700, 128)])
+def test_items_out_of_range_are_refused_in_the_forward(cuda_lib, table, fields, lens, d):
+    """An item whose rows, keys, head or slot are not the plan's is skipped and reported: its own CTA's
+    first item, and one that a CTA takes behind another (700 sequences: several items to an SM)."""
+    sla = cuda_lib
+    case = (lens, None, 4, 2, d, True)
+    q, k, v, _, lq, _ = make(case, seed=20)
+    want = sla.prompt_attention(q.cuda(), k.cuda(), v.cuda(), plan_of(sla, case))
+    plan = plan_of(sla, case)
+    from tests.test_prompt import read
+
+    items = read(plan)[1]
+    at = len(items) - 1
+    fields = {n: sum(lq) if n == "q0" else x for n, x in fields.items()}
+    h = broken(plan, table, at, **fields)
+    assert h.n_slots == 0 and (len(items) > 4 * 148) == (len(lens) > 1)
+    out = torch.full_like(want, 7.0)
+    sla.prompt_forward(q.cuda(), k.cuda(), v.cuda(), plan, out=out)
+    assert sla.read_device_status(plan.device_bytes) == sla.SLA_ERR_DEVICE_CHECK
+    it = items[at]
+    rows, heads = slice(it["q0"], it["q0"] + it["nq"]), slice(it["head"] * 2, it["head"] * 2 + 2)
+    assert (out[rows, heads] == 7.0).all()
+    if len(lens) == 1:  # (behind a bad item a CTA takes no more: those run as blocks of their own)
+        want[rows, heads] = 7.0
+        assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("table,fields", [("items", dict(slot=1 << 20)), ("items", dict(head=1)), ("joins", dict(head=1)),
+                                          ("joins", dict(first=1)), ("joins", dict(n=1 << 20)), ("joins", dict(q0=-1))], ids=str)
+def test_pieces_out_of_range_are_refused(cuda_lib, table, fields):
+    sla = cuda_lib
+    case = ([1], [9000], 8, 1, 128, True)
+    q, k, v, _, _, _ = make(case, seed=21)
+    plan = plan_of(sla, case)
+    assert broken(plan, table, 0, **fields).n_joins == 1
+    out = torch.full((1, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(plan.workspace_size, dtype=torch.uint8, device="cuda")  # a piece that is not written: weight 1, zeros
+    sla.prompt_forward(q.cuda(), k.cuda(), v.cuda(), plan, out=out, workspace=ws)
+    assert sla.read_device_status(plan.device_bytes) == sla.SLA_ERR_DEVICE_CHECK
+    assert (out == 7.0).all() == (table == "joins")
+
+
+@pytest.mark.parametrize("table,fields", [("keys", dict(head=2)), ("keys", dict(slot=1 << 20)), ("keys", dict(t1=1000)),
+                                          ("keys", dict(t0=-1)), ("keys", dict(block=100)), ("rows", dict(head=2)), ("rows", dict(head=-1)),
+                                          ("rows", dict(nq=0)), ("kjoins", dict(head=2)), ("kjoins", dict(first=-1)),
+                                          ("kjoins", dict(n=1 << 20)), ("kjoins", dict(row=-1)), ("kjoins", dict(row=2500))], ids=str)
+def test_items_out_of_range_are_refused_in_the_backward(cuda_lib, table, fields):
+    from tests.test_prompt import read
+
+    sla = cuda_lib
+    case = ([2500], None, 4, 2, 64, True)
+    q, k, v, do, _, _ = make(case, seed=22)
+    q, k, v, do = q.cuda(), k.cuda(), v.cuda(), do.cuda()
+    good = plan_of(sla, case)
+    o, lse = sla.prompt_forward(q, k, v, good)
+    ws = torch.zeros(good.backward_workspace_size, dtype=torch.uint8, device="cuda")
+    want = sla.prompt_backward(q, k, v, o, lse, do, good, workspace=ws)
+    plan = plan_of(sla, case)
+    h = broken(plan, table, 0, **fields)
+    assert h.n_kjoins > 0
+    got = [torch.full_like(t, 7.0) for t in (q, k, v)]
+    sla.prompt_backward(q, k, v, o, lse, do, plan, out=tuple(got), workspace=ws)
+    assert sla.read_device_status(plan.device_bytes) == sla.SLA_ERR_DEVICE_CHECK
+    _, _, _, keys, kjoins, rows = read(good)
+    if table == "rows":
+        it = rows[0]
+        want[0][it["q0"]:it["q0"] + it["nq"], it["head"] * 2:it["head"] * 2 + 2] = 7.0
+    elif table == "kjoins":
+        it = kjoins[0]
+        for t in want[1:]:
+            t[it["row"]:it["row"] + it["nk"], it["head"]] = 7.0
+    elif keys[0]["slot"] < 0:
+        it = keys[0]
+        for t in want[1:]:
+            t[it["block"] * 128:it["block"] * 128 + 128, it["head"]] = 7.0
+    # (a split key tile's piece that is skipped leaves what the call before left in its slot: the same sums)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
