@@ -44,6 +44,14 @@ void record_use(const Tensor& kept, cudaStream_t home) {
   if (now.stream() != home) kept.record_stream(now);
 }
 
+// The autograd functions here have no forward-mode derivative. A dual tensor need not require grad,
+// so it is looked for by its tangent.
+template <typename... Ts>
+void refuse_tangents(const char* call, const Ts&... xs) {
+  const bool dual = ((xs.defined() && xs._fw_grad(/*level=*/0).defined()) || ...);
+  TORCH_CHECK_NOT_IMPLEMENTED(!dual, call, " has no forward-mode derivative");
+}
+
 // ---------------------------------------------------------------------------
 // rotary positions
 // ---------------------------------------------------------------------------
@@ -205,6 +213,7 @@ Tensor rope(const Tensor& x, const TablePtr& table, const OptTensor& positions, 
             const OptTensor& out, bool inverse) {
   check_heads(x, "x");
   dtype_code(x, "x");
+  refuse_tangents("rope", x, out ? *out : Tensor());
   c10::cuda::CUDAGuard guard(x.device());
   const int64_t n = count_of(x, N);
   const Tensor pos = positions ? *positions : Tensor();
@@ -329,6 +338,7 @@ std::tuple<Tensor, Tensor> qk_norm_rope(const Tensor& q, const Tensor& k, const 
                                         const TablePtr& table, const OptTensor& positions, double eps, const OptInt& N,
                                         const OptInt& rows, const std::optional<std::tuple<Tensor, Tensor>>& out) {
   check_pair(q, k, wq, wk);
+  refuse_tangents("qk_norm_rope", q, k, wq, wk, out ? std::get<0>(*out) : Tensor(), out ? std::get<1>(*out) : Tensor());
   c10::cuda::CUDAGuard guard(q.device());
   const int64_t n = count_of(q, N);
   const Tensor pos = positions ? *positions : Tensor();
@@ -510,6 +520,7 @@ std::tuple<Tensor, Tensor, Tensor> prompt_backward(const Tensor& q, const Tensor
 }
 
 Tensor prompt_attention(const Tensor& q, const Tensor& k, const Tensor& v, const PlanPtr& plan) {
+  refuse_tangents("prompt_attention", q, k, v);
   c10::OptionalDeviceGuard guard(plan->device.device());
   if (at::GradMode::is_enabled() && (q.requires_grad() || k.requires_grad() || v.requires_grad())) {
     check_grad(*plan);

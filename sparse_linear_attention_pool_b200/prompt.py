@@ -103,7 +103,7 @@ def prompt_backward(q, k, v, o, lse, do, plan: PromptPlan, *, rest=None, out=Non
 
 def prompt_attention(q, k, v, plan: PromptPlan, *, stream=None):
     """O = softmax(scale Q K^T + mask) V for the plan's packed sequences, [rows of q, Hq, d].
-    Differentiable in q, k and v (with a plan made for it)."""
+    Differentiable in q, k and v (with a plan made for it), in reverse mode."""
     if stream is not None:
         with on_stream(stream, q.device, q, k, v):
             return _sla.prompt_attention(q, k, v, plan._c)

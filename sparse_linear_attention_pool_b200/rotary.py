@@ -8,7 +8,8 @@ in the same pass: the binding of sla_rope and sla_qk_norm_rope.
 Tensors are head rows [B, H, N, d] in any memory order with contiguous rows (a
 projection's [B, N, H, d] output goes in as x.transpose(1, 2)), or packed tokens
 [T, H, d]; bfloat16, float16 or float32. Outputs are contiguous in the same
-logical shape. Both calls are differentiable: in the inputs and the weights.
+logical shape. Both calls are differentiable in the inputs and the weights, in reverse
+mode (forward-mode dual tensors are refused).
 """
 from __future__ import annotations
 

@@ -111,3 +111,23 @@ def test_memory_outlives_a_call_on_another_stream(cuda_lib):
         assert not side.query(), i  # else nothing was tested
         assert not {p for *_, p in sizes} & {t.data_ptr() for t in again}, i
         torch.cuda.synchronize()
+
+
+def test_forward_mode_is_refused(cuda_lib):
+    """There is no forward-mode derivative: a dual tensor is refused, not stripped of its tangent."""
+    sla = cuda_lib
+    fwd = torch.autograd.forward_ad
+    x, t = randn(5, 2, 64, seed=1), randn(5, 2, 64, seed=2)
+    w = torch.ones(64, device="cuda", dtype=torch.bfloat16)
+    table, plan = sla.rope_table(64), sla.prompt_plan([5], Hq=2, Hkv=2, d=64)
+    with fwd.dual_level():
+        dual, dual_w = fwd.make_dual(x, t), fwd.make_dual(w, w)
+        for call in (lambda: sla.rope(dual, table), lambda: sla.rope(x, table, out=fwd.make_dual(x.clone(), t)),
+                     lambda: sla.qk_norm_rope(dual, x, w, w), lambda: sla.qk_norm_rope(x, dual, w, w),
+                     lambda: sla.qk_norm_rope(x, x, dual_w, w), lambda: sla.qk_norm_rope(x, x, w, dual_w),
+                     lambda: sla.prompt_attention(dual, x, x, plan), lambda: sla.prompt_attention(x, dual, x, plan),
+                     lambda: sla.prompt_attention(x, x, dual, plan)):
+            with pytest.raises(NotImplementedError):
+                call()
+        sla.rope(x, table), sla.prompt_attention(x, x, x, plan)  # others go on inside the level
+    sla.rope(x, table)
