@@ -52,6 +52,12 @@ void refuse_tangents(const char* call, const Ts&... xs) {
   TORCH_CHECK_NOT_IMPLEMENTED(!dual, call, " has no forward-mode derivative");
 }
 
+// A kernel wrote to a caller's tensor: autograd is told, as by torch's own operations in place, so that
+// a backward which saved the old values is refused.
+void written(const Tensor& out) {
+  if (!out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
+}
+
 // ---------------------------------------------------------------------------
 // rotary positions
 // ---------------------------------------------------------------------------
@@ -228,7 +234,9 @@ Tensor rope(const Tensor& x, const TablePtr& table, const OptTensor& positions, 
     meta->pos = pos;
     return RopeFunction::apply(x, meta);
   }
-  return run_rope(x, *table, pos, n, out_for(x, out, rows, n), inverse);
+  const Tensor y = run_rope(x, *table, pos, n, out_for(x, out, rows, n), inverse);
+  if (out) written(y);
+  return y;
 }
 
 // ---------------------------------------------------------------------------
@@ -357,6 +365,7 @@ std::tuple<Tensor, Tensor> qk_norm_rope(const Tensor& q, const Tensor& k, const 
   const Tensor yq = out_for(q, out ? OptTensor(std::get<0>(*out)) : OptTensor(), rows, n);
   const Tensor yk = out_for(k, out ? OptTensor(std::get<1>(*out)) : OptTensor(), rows, n);
   run_norm(q, k, wq, wk, table, pos, float(eps), n, yq, yk);
+  if (out) written(yq), written(yk);
   return {yq, yk};
 }
 
@@ -503,6 +512,7 @@ std::tuple<Tensor, OptTensor, OptTensor> prompt_forward(const Tensor& q, const T
   at::NoGradGuard no_grad;
   c10::OptionalDeviceGuard guard(plan->device.device());
   auto [o, lse, rest] = run_forward(q, k, v, *plan, out ? *out : Tensor(), want_lse, want_rest, workspace);
+  if (out) written(o);
   return {o, want_lse ? OptTensor(lse) : OptTensor(), want_rest ? OptTensor(rest) : OptTensor()};
 }
 
@@ -516,7 +526,9 @@ std::tuple<Tensor, Tensor, Tensor> prompt_backward(const Tensor& q, const Tensor
   c10::OptionalDeviceGuard guard(plan->device.device());
   Tensor dq, dk, dv;
   if (out) std::tie(dq, dk, dv) = *out;
-  return run_backward(q, k, v, o, lse, rest ? *rest : Tensor(), dO, *plan, dq, dk, dv, workspace);
+  const auto made = run_backward(q, k, v, o, lse, rest ? *rest : Tensor(), dO, *plan, dq, dk, dv, workspace);
+  if (out) written(dq), written(dk), written(dv);
+  return made;
 }
 
 Tensor prompt_attention(const Tensor& q, const Tensor& k, const Tensor& v, const PlanPtr& plan) {

@@ -131,3 +131,39 @@ def test_forward_mode_is_refused(cuda_lib):
                 call()
         sla.rope(x, table), sla.prompt_attention(x, x, x, plan)  # others go on inside the level
     sla.rope(x, table)
+
+
+def out_calls(sla):
+    """(operator, its `out` tensors, the call) of every call that writes to the caller's tensors."""
+    x, w = randn(5, 2, 64, seed=1), torch.ones(64, device="cuda", dtype=torch.bfloat16)
+    table, plan = sla.rope_table(64), sla.prompt_plan([5], Hq=2, Hkv=2, d=64)
+    o, lse = sla.prompt_forward(x, x, x, plan)
+    new = lambda n: [torch.zeros_like(x) for _ in range(n)]  # noqa: E731
+    return [("rope", new(1), lambda t: sla.rope(x, table, out=t[0])),
+            ("qk_norm_rope", new(2), lambda t: sla.qk_norm_rope(x, x, w, w, table, out=tuple(t))),
+            ("prompt_forward", new(1), lambda t: sla.prompt_forward(x, x, x, plan, out=t[0])),
+            ("prompt_backward", new(3), lambda t: sla.prompt_backward(x, x, x, o, lse, x, plan, out=tuple(t)))]
+
+
+def test_writes_to_out_are_seen_by_autograd(cuda_lib):
+    """A tensor that another operation saved for its backward and that `out` overwrites is noticed."""
+    sla = cuda_lib
+    for name, outs, call in out_calls(sla):
+        for i in range(len(outs)):
+            leaf = torch.ones(5, 2, 64, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+            y = (leaf * outs[i]).sum()
+            before = outs[i]._version
+            call(outs)
+            assert outs[i]._version > before, name
+            with pytest.raises(RuntimeError, match="inplace"):
+                y.backward()
+    # in place: the input's own version
+    x, table = randn(5, 2, 64, seed=1), sla.rope_table(64)
+    before = x._version
+    sla.rope(x, table, out=x)
+    assert x._version > before
+    # without autograd's bookkeeping there is none to keep
+    with torch.inference_mode():
+        y = torch.empty_like(x)
+        sla.rope(x, table, out=y)
+    sla.rope(x, table, out=y)
