@@ -57,6 +57,10 @@ void refuse_tangents(const char* call, const Ts&... xs) {
 void written(const Tensor& out) {
   if (!out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
 }
+// What the call writes there would not be what autograd holds it for.
+void check_out(const Tensor& out) {
+  TORCH_CHECK_VALUE(!(at::GradMode::is_enabled() && out.requires_grad()), "out: a tensor that requires grad");
+}
 
 // ---------------------------------------------------------------------------
 // rotary positions
@@ -234,6 +238,7 @@ Tensor rope(const Tensor& x, const TablePtr& table, const OptTensor& positions, 
     meta->pos = pos;
     return RopeFunction::apply(x, meta);
   }
+  if (out) check_out(*out);
   const Tensor y = run_rope(x, *table, pos, n, out_for(x, out, rows, n), inverse);
   if (out) written(y);
   return y;
@@ -362,6 +367,7 @@ std::tuple<Tensor, Tensor> qk_norm_rope(const Tensor& q, const Tensor& k, const 
     const auto y = NormFunction::apply(q, k, wq, wk, meta);
     return {y[0], y[1]};
   }
+  if (out) check_out(std::get<0>(*out)), check_out(std::get<1>(*out));
   const Tensor yq = out_for(q, out ? OptTensor(std::get<0>(*out)) : OptTensor(), rows, n);
   const Tensor yk = out_for(k, out ? OptTensor(std::get<1>(*out)) : OptTensor(), rows, n);
   run_norm(q, k, wq, wk, table, pos, float(eps), n, yq, yk);
@@ -509,6 +515,7 @@ struct PromptFunction : torch::autograd::Function<PromptFunction> {
 std::tuple<Tensor, OptTensor, OptTensor> prompt_forward(const Tensor& q, const Tensor& k, const Tensor& v,
                                                         const PlanPtr& plan, const OptTensor& out, bool want_lse,
                                                         bool want_rest, const OptTensor& workspace) {
+  if (out) check_out(*out);
   at::NoGradGuard no_grad;
   c10::OptionalDeviceGuard guard(plan->device.device());
   auto [o, lse, rest] = run_forward(q, k, v, *plan, out ? *out : Tensor(), want_lse, want_rest, workspace);
@@ -521,11 +528,14 @@ std::tuple<Tensor, Tensor, Tensor> prompt_backward(const Tensor& q, const Tensor
                                                    const PlanPtr& plan,
                                                    const std::optional<std::tuple<Tensor, Tensor, Tensor>>& out,
                                                    const OptTensor& workspace) {
+  Tensor dq, dk, dv;
+  if (out) {
+    std::tie(dq, dk, dv) = *out;
+    for (const Tensor* t : {&dq, &dk, &dv}) check_out(*t);
+  }
   at::NoGradGuard no_grad;
   check_grad(*plan);
   c10::OptionalDeviceGuard guard(plan->device.device());
-  Tensor dq, dk, dv;
-  if (out) std::tie(dq, dk, dv) = *out;
   const auto made = run_backward(q, k, v, o, lse, rest ? *rest : Tensor(), dO, *plan, dq, dk, dv, workspace);
   if (out) written(dq), written(dk), written(dv);
   return made;

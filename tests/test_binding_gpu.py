@@ -167,3 +167,16 @@ def test_writes_to_out_are_seen_by_autograd(cuda_lib):
         y = torch.empty_like(x)
         sla.rope(x, table, out=y)
     sla.rope(x, table, out=y)
+
+
+def test_out_that_requires_grad_is_refused(cuda_lib):
+    sla = cuda_lib
+    for name, outs, call in out_calls(sla):
+        for i in range(len(outs)):
+            some = [t.requires_grad_(True) if i == j else t for j, t in enumerate(torch.zeros_like(t) for t in outs)]
+            with pytest.raises(ValueError, match="requires grad"):
+                call(some)
+            with torch.no_grad():
+                before = some[i]._version
+                call(some)
+            assert some[i]._version > before, name
