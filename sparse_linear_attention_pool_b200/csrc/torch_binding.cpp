@@ -8,6 +8,7 @@
 #include <torch/extension.h>
 
 #include <cstring>
+#include <limits>
 #include <string>
 #include <vector>
 
@@ -104,11 +105,14 @@ sla_heads heads_of(const Tensor& x) {
   return {x.data_ptr(), int(x.size(1)), 0, x.stride(1), x.stride(0)};
 }
 
-int64_t count_of(const Tensor& x, const OptInt& N) {
+// The tokens that a call takes; sizes that the library's int parameters would cut are refused.
+int64_t count_of(const Tensor& x, const OptInt& N, const char* call) {
   const int64_t n = tokens(x);
-  if (!N) return n;
-  TORCH_CHECK_VALUE(*N >= 0 && *N <= n, "N must be 0 .. ", n);
-  return *N;
+  TORCH_CHECK_VALUE(!N || (*N >= 0 && *N <= n), "N must be 0 .. ", n);
+  const int64_t taken = N ? *N : n;
+  for (int64_t size : {batch(x), taken, x.size(1), x.size(-1)})
+    if (size > std::numeric_limits<int>::max()) throw StatusError(SLA_ERR_UNSUPPORTED, call);
+  return taken;
 }
 
 // The rotation of a call, positions checked against B and N; `pos` may be undefined.
@@ -225,7 +229,7 @@ Tensor rope(const Tensor& x, const TablePtr& table, const OptTensor& positions, 
   dtype_code(x, "x");
   refuse_tangents("rope", x, out ? *out : Tensor());
   c10::cuda::CUDAGuard guard(x.device());
-  const int64_t n = count_of(x, N);
+  const int64_t n = count_of(x, N, "sla_rope");
   const Tensor pos = positions ? *positions : Tensor();
   if (at::GradMode::is_enabled() && x.requires_grad()) {
     TORCH_CHECK_VALUE(!out, "out cannot be given for a tensor that requires grad");
@@ -353,7 +357,8 @@ std::tuple<Tensor, Tensor> qk_norm_rope(const Tensor& q, const Tensor& k, const 
   check_pair(q, k, wq, wk);
   refuse_tangents("qk_norm_rope", q, k, wq, wk, out ? std::get<0>(*out) : Tensor(), out ? std::get<1>(*out) : Tensor());
   c10::cuda::CUDAGuard guard(q.device());
-  const int64_t n = count_of(q, N);
+  const int64_t n = count_of(q, N, "sla_qk_norm_rope");
+  count_of(k, N, "sla_qk_norm_rope");
   const Tensor pos = positions ? *positions : Tensor();
   if (at::GradMode::is_enabled() &&
       (q.requires_grad() || k.requires_grad() || wq.requires_grad() || wk.requires_grad())) {
@@ -382,7 +387,8 @@ std::tuple<Tensor, Tensor, OptTensor, OptTensor> qk_norm_rope_backward(
   at::NoGradGuard no_grad;
   check_pair(q, k, wq, wk);
   c10::cuda::CUDAGuard guard(q.device());
-  const int64_t n = count_of(q, N);
+  const int64_t n = count_of(q, N, "sla_qk_norm_rope_backward");
+  count_of(k, N, "sla_qk_norm_rope_backward");
   const Tensor* pairs[2][2] = {{&dyq, &q}, {&dyk, &k}};
   for (auto& p : pairs) {
     check_like(*p[0], *p[1], "dyq and dyk");

@@ -180,3 +180,20 @@ def test_out_that_requires_grad_is_refused(cuda_lib):
                 before = some[i]._version
                 call(some)
             assert some[i]._version > before, name
+
+
+def test_counts_past_32_bits_are_refused(cuda_lib):
+    """Views of one token or one head, repeated: no count is cut to its low 32 bits."""
+    sla = cuda_lib
+    table = sla.rope_table(2)
+    w = torch.ones(2, device="cuda")
+    one = torch.ones(1, 1, 2, device="cuda", dtype=torch.bfloat16)
+    for x in (one.expand(2 ** 32 + 5, 1, 2), one[None].expand(1, 1, 2 ** 32 + 5, 2), one[None].expand(2 ** 32 + 1, 1, 1, 2),
+              one.expand(1, 2 ** 32 + 1, 2)):
+        for call in (lambda: sla.rope(x, table), lambda: sla.qk_norm_rope(x, x, w, w, table),
+                     lambda: sla.qk_norm_rope_backward(x, x, w, w, x, x, table)):
+            with pytest.raises(sla.SLAError) as e:
+                call()
+            assert e.value.status == sla.SLA_ERR_UNSUPPORTED
+    # the first tokens of a long view are not many
+    assert sla.rope(one.expand(2 ** 20, 1, 2), table, N=3, out=torch.empty(3, 1, 2, device="cuda", dtype=torch.bfloat16)).shape == (3, 1, 2)
