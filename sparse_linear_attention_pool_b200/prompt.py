@@ -18,7 +18,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import PromptParams, SLAError, load
+from . import SLA_ERR_INVALID_ARG, SLA_ERR_UNSUPPORTED, PromptParams, SLAError, load
 from .rotary import _sla, on_stream
 
 
@@ -60,8 +60,14 @@ def prompt_plan(lens_q: Sequence[int], lens_k: Optional[Sequence[int]] = None, *
     if len(lens_k) != len(lens_q):
         raise ValueError("lens_q and lens_k name different numbers of sequences")
     n = len(lens_q)
+    Hq, Hkv, d = int(Hq), int(Hkv), int(d)
+    # 32-bit fields of the struct, which cut what does not fit them
+    if any(not -0x80000000 <= x <= 0x7fffffff for x in (Hq, Hkv, d, n)):
+        raise SLAError(SLA_ERR_UNSUPPORTED, "sla_prompt_plan")
+    if softmax_scale != 0.0 and abs(softmax_scale) < 1e-30:
+        raise SLAError(SLA_ERR_INVALID_ARG, "sla_prompt_plan")
     aq, ak = (ctypes.c_int32 * n)(*lens_q), (ctypes.c_int32 * n)(*lens_k)
-    p = PromptParams(n, ctypes.addressof(aq), ctypes.addressof(ak), int(Hq), int(Hkv), int(d), int(bool(causal)),
+    p = PromptParams(n, ctypes.addressof(aq), ctypes.addressof(ak), Hq, Hkv, d, int(bool(causal)),
                      int(grad), float(softmax_scale))
     lib = load()
     st = lib.sla_prompt_validate(p)
@@ -72,8 +78,8 @@ def prompt_plan(lens_q: Sequence[int], lens_k: Optional[Sequence[int]] = None, *
     if st:
         raise SLAError(st, "sla_prompt_plan")
     host = (ctypes.c_char * lib.sla_prompt_plan_used(words)).from_buffer(words)
-    return PromptPlan(host, torch.frombuffer(host, dtype=torch.uint8).to(device, copy=True), lens_q, lens_k, int(Hq),
-                      int(Hkv), int(d), bool(causal), grad)
+    return PromptPlan(host, torch.frombuffer(host, dtype=torch.uint8).to(device, copy=True), lens_q, lens_k, Hq, Hkv, d,
+                      bool(causal), grad)
 
 
 def prompt_forward(q, k, v, plan: PromptPlan, *, out=None, want_lse: bool = True, want_rest: bool = False,

@@ -259,3 +259,20 @@ def test_binding_refuses_cpu_tensors():
     x = torch.zeros(5, 1, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         sla.prompt_attention(x, x, x, plan)
+
+
+@pytest.mark.parametrize("kw", [dict(Hq=2 ** 32 + 4), dict(Hkv=2 ** 32 + 2), dict(d=2 ** 32 + 64), dict(Hq=2 ** 31), dict(Hq=-2 ** 33)], ids=str)
+def test_plan_sizes_past_32_bits_are_refused(lib, kw):
+    """No size is cut to its low 32 bits."""
+    a = dict(Hq=4, Hkv=2, d=64, device="cpu")
+    with pytest.raises(sla.SLAError) as e:
+        sla.prompt_plan([5], **{**a, **kw})
+    assert e.value.status == sla.SLA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("scale", [1e-46, -1e-46, 1e-31])
+def test_a_scale_that_float32_rounds_to_nothing_is_refused(lib, scale):
+    """It would select the default."""
+    with pytest.raises(sla.SLAError) as e:
+        sla.prompt_plan([5], Hq=4, Hkv=2, d=64, softmax_scale=scale, device="cpu")
+    assert e.value.status == sla.SLA_ERR_INVALID_ARG
