@@ -526,3 +526,39 @@ def test_items_out_of_range_are_refused_in_the_backward(cuda_lib, table, fields)
             t[it["block"] * 128:it["block"] * 128 + 128, it["head"]] = 7.0
     # (a split key tile's piece that is skipped leaves what the call before left in its slot: the same sums)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_infinite_score_makes_its_rows_nan(cuda_lib, d):
+    """Whatever column of a block the key stands in: softmax of an infinite score is NaN, not infinity."""
+    sla = cuda_lib
+    case = ([40], None, 2, 1, d, False)
+    q, k, v, _, _, _ = make(case, seed=18)
+    q[..., 0] = 1.0
+    plan = plan_of(sla, case)
+    for j in range(32):
+        bad = k.clone()
+        bad[j, 0, 0] = math.inf
+        o, lse = sla.prompt_forward(q.cuda(), bad.cuda(), v.cuda(), plan)
+        assert o.isnan().all() and not torch.isfinite(lse).any(), j
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_nan_query_makes_its_keys_gradients_nan(cuda_lib, d):
+    """dV of every key that the query sees, whatever column of the tile it stands in, and of no other."""
+    sla = cuda_lib
+    case = ([200], None, 1, 1, d, True)
+    q, k, v, do, _, _ = make(case, seed=19)
+    plan = plan_of(sla, case)
+
+    def grads(q):
+        o, lse = sla.prompt_forward(q, k.cuda(), v.cuda(), plan)
+        return sla.prompt_backward(q, k.cuda(), v.cuda(), o, lse, do.cuda(), plan)
+
+    clean = grads(q.cuda())
+    for r in [*range(100, 116), 0, 127, 128, 199]:
+        bad = q.cuda()
+        bad[r] = math.nan
+        dq, dk, dv = grads(bad)
+        assert dq[r].isnan().all() and dk[:r + 1].isnan().all() and dv[:r + 1].isnan().all(), r
+        assert torch.equal(dv[r + 1:], clean[2][r + 1:]), r
