@@ -46,9 +46,9 @@ struct PromptDev {
   long long o_row, o_head;
   __nv_bfloat16* rest;
   float *lse, *part, *part_lse;
-  int Hq, Hkv, G, tpt, box, causal, tiles;  // box: tokens that a copy of Q brings
-  int n_slots;
+  int Hq, G, tpt, box, causal, tiles;  // box: tokens that a copy of Q brings
   long long Tq, Tk;
+  int n_slots;
   float scale_log2;
 };
 
@@ -122,10 +122,10 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, FEW>::kThreads, FwdCfg<D, TIL
   __shared__ int abort_sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* status = reinterpret_cast<int*>(a.plan_dev);
-  auto sound = [&](const PromptItem& it) {
+  auto sound = [&](const PromptItem& it) {  // (heads fit 16 bits)
     return it.q0 >= 0 && it.nq >= 1 && it.k0 >= 0 && it.lk >= 0 && it.q0 + (long long)it.nq <= a.Tq &&
            it.k0 + (long long)it.lk <= a.Tk && it.nq <= TILES * a.tpt && (!FEW || it.nq <= a.box) && it.b0 >= 0 &&
-           it.head >= 0 && it.head < a.Hkv && it.slot < a.n_slots;
+           uint32_t(it.head) < 65536u && it.head * a.G < a.Hq && it.slot < a.n_slots;
   };
   auto work_of = [&](const PromptItem& it) {
     auto end_block = [&](int t) {
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const PromptDev a) {
   const int t = r >> 7, rr = r & 127;
   const int tok = t * a.tpt + rr / a.G, g = rr - (rr / a.G) * a.G;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
-  if (jn.q0 < 0 || jn.head < 0 || jn.head >= a.Hkv || jn.first < 0 || jn.n < 0 || jn.first + (long long)jn.n > a.n_slots) {
+  if (jn.q0 < 0 || jn.head < 0 || jn.head * (long long)a.G >= a.Hq || jn.first < 0 || jn.n < 0 || jn.first + (long long)jn.n > a.n_slots) {
     if (threadIdx.x == 0) atomicExch(reinterpret_cast<int*>(a.plan_dev), kDevBadIndex);
     return;
   }
@@ -707,7 +707,6 @@ cudaError_t launch_prompt_forward(const PromptArgs& a, cudaStream_t s) {
   v.part = a.part;
   v.part_lse = a.part_lse;
   v.Hq = p.Hq;
-  v.Hkv = p.Hkv;
   v.n_slots = p.n_slots;
   v.G = p.G;
   v.tpt = kPromptTile / p.G;
