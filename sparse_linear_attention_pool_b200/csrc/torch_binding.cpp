@@ -45,6 +45,12 @@ void record_use(const Tensor& kept, cudaStream_t home) {
   if (now.stream() != home) kept.record_stream(now);
 }
 
+// A caller's scratch: the library sees its address and its bytes alone.
+void check_workspace(const OptTensor& w, const at::Device& device) {
+  TORCH_CHECK_VALUE(!w || (w->is_cuda() && w->device() == device && w->is_contiguous()),
+                    "workspace: a contiguous tensor on the inputs' device");
+}
+
 // The autograd functions here have no forward-mode derivative. A dual tensor need not require grad,
 // so it is looked for by its tangent.
 template <typename... Ts>
@@ -385,6 +391,7 @@ std::tuple<Tensor, Tensor, OptTensor, OptTensor> qk_norm_rope_backward(
     const TablePtr& table, const OptTensor& positions, double eps, const OptInt& N, bool want_w,
     const OptTensor& workspace) {
   at::NoGradGuard no_grad;
+  check_workspace(workspace, q.device());
   check_pair(q, k, wq, wk);
   c10::cuda::CUDAGuard guard(q.device());
   const int64_t n = count_of(q, N, "sla_qk_norm_rope_backward");
@@ -522,6 +529,7 @@ std::tuple<Tensor, OptTensor, OptTensor> prompt_forward(const Tensor& q, const T
                                                         const PlanPtr& plan, const OptTensor& out, bool want_lse,
                                                         bool want_rest, const OptTensor& workspace) {
   if (out) check_out(*out);
+  check_workspace(workspace, plan->device.device());
   at::NoGradGuard no_grad;
   c10::OptionalDeviceGuard guard(plan->device.device());
   auto [o, lse, rest] = run_forward(q, k, v, *plan, out ? *out : Tensor(), want_lse, want_rest, workspace);
@@ -539,6 +547,7 @@ std::tuple<Tensor, Tensor, Tensor> prompt_backward(const Tensor& q, const Tensor
     std::tie(dq, dk, dv) = *out;
     for (const Tensor* t : {&dq, &dk, &dv}) check_out(*t);
   }
+  check_workspace(workspace, plan->device.device());
   at::NoGradGuard no_grad;
   check_grad(*plan);
   c10::OptionalDeviceGuard guard(plan->device.device());

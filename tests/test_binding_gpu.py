@@ -197,3 +197,22 @@ def test_counts_past_32_bits_are_refused(cuda_lib):
             assert e.value.status == sla.SLA_ERR_UNSUPPORTED
     # the first tokens of a long view are not many
     assert sla.rope(one.expand(2 ** 20, 1, 2), table, N=3, out=torch.empty(3, 1, 2, device="cuda", dtype=torch.bfloat16)).shape == (3, 1, 2)
+
+
+def test_workspaces_are_checked(cuda_lib):
+    """A workspace on the host, or one whose bytes are not in one piece, is refused before a launch."""
+    sla = cuda_lib
+    x, w = randn(6, 2, 64, seed=1), torch.ones(64, device="cuda", dtype=torch.bfloat16)
+    k = torch.zeros(9000, 2, 64, device="cuda", dtype=torch.bfloat16)
+    one, plan = sla.prompt_plan([1], [9000], Hq=2, Hkv=2, d=64), sla.prompt_plan([6], Hq=2, Hkv=2, d=64)
+    assert one.workspace_size > 0
+    o, lse = sla.prompt_forward(x, x, x, plan)
+    for n, call in ((one.workspace_size, lambda ws: sla.prompt_forward(x[:1], k, k, one, workspace=ws)),
+                    (plan.backward_workspace_size, lambda ws: sla.prompt_backward(x, x, x, o, lse, x, plan, workspace=ws)),
+                    (1 << 20, lambda ws: sla.qk_norm_rope_backward(x, x, w, w, x, x, workspace=ws))):
+        for bad in (torch.zeros(n, dtype=torch.uint8), torch.zeros(n, dtype=torch.uint8).pin_memory(),
+                    torch.zeros(2 * n, dtype=torch.uint8, device="cuda")[::2],
+                    torch.zeros(1, dtype=torch.uint8, device="cuda").expand(n)):
+            with pytest.raises(ValueError, match="workspace"):
+                call(bad)
+        call(torch.zeros(n, dtype=torch.uint8, device="cuda"))

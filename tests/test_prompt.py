@@ -276,3 +276,17 @@ def test_a_scale_that_float32_rounds_to_nothing_is_refused(lib, scale):
     with pytest.raises(sla.SLAError) as e:
         sla.prompt_plan([5], Hq=4, Hkv=2, d=64, softmax_scale=scale, device="cpu")
     assert e.value.status == sla.SLA_ERR_INVALID_ARG
+
+
+def test_binding_refuses_a_workspace_on_the_host():
+    """Before anything else of the call: the library would take its address for the device's."""
+    plan = sla.prompt_plan([5], Hq=1, Hkv=1, d=64, device="cpu")
+    x, ws = torch.zeros(5, 1, 64, dtype=torch.bfloat16), torch.zeros(1 << 16, dtype=torch.uint8)
+    lse = torch.zeros(5, 1)
+    with pytest.raises(ValueError, match="workspace"):
+        sla.prompt_forward(x, x, x, plan, workspace=ws)
+    with pytest.raises(ValueError, match="workspace"):
+        sla.prompt_backward(x, x, x, x, lse, x, plan, workspace=ws)
+    w = torch.ones(64)
+    with pytest.raises(ValueError, match="workspace"):
+        sla.qk_norm_rope_backward(x, x, w, w, x, x, workspace=ws)
