@@ -50,7 +50,8 @@ def rope_frequencies(rot_dim: int, *, theta: float = 10000.0, sections: Optional
                 factor, the fastest keeps its frequency;
       "yarn"    pairs that turn more than beta_fast times over `original` positions keep
                 their frequency, those below beta_slow turns are divided by factor, with a
-                linear ramp between, and cos and sin are scaled by 0.1 ln(factor) + 1.
+                linear ramp between, and cos and sin are scaled by 0.1 ln(factor) + 1 (by 1
+                for a factor of at most 1).
     """
     if rot_dim < 0 or rot_dim % 2:
         raise ValueError("rot_dim must be even and not negative")
@@ -78,7 +79,7 @@ def rope_frequencies(rot_dim: int, *, theta: float = 10000.0, sections: Optional
             lo, hi = max(0, math.floor(pair_of(beta_fast))), min(2 * n - 1, math.ceil(pair_of(beta_slow)))
             ramp = [min(1.0, max(0.0, (i - lo) / max(hi - lo, 0.001))) for i in range(n)]
             f = [x * (1.0 - r) + x / factor * r for x, r in zip(f, ramp)]
-            gain = 0.1 * math.log(factor) + 1.0
+            gain = 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
         freqs += f
         axes += [a] * n
     return freqs, axes, gain

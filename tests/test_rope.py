@@ -174,3 +174,11 @@ def test_binding_refuses_cpu_tensors():
 
 def test_struct_sizes_match_the_header():
     assert ctypes.sizeof(sla.Heads) == 40 and ctypes.sizeof(sla.RopeSpec) == 72
+
+
+def test_yarn_scales_cos_and_sin_only_for_longer_contexts():
+    """The factor on cos and sin is 0.1 ln(factor) + 1 above 1, and 1 where nothing is stretched."""
+    for factor, gain in ((8.0, 0.1 * math.log(8.0) + 1.0), (1.0, 1.0), (0.5, 1.0), (0.01, 1.0)):
+        f, _, g = rope_frequencies(128, scaling="yarn", factor=factor, original=4096)
+        assert g == pytest.approx(gain, rel=1e-15)
+        assert sla.rope_table(128, scaling="yarn", factor=factor, original=4096, device="cpu").gain == g
