@@ -6,10 +6,10 @@
 //
 // The angle. f_i / 2 pi is held as a 64-bit fixed-point fraction of a turn, so
 // p f_i mod one turn is one 64-bit integer product mod 2^64: exact for every
-// position (its error is p 2^-65 turns, from the table), where a float32
+// position (its error is p 2^-65 turns, from the table's rounding), where a float32
 // product is off by p f_i 2^-24 radians - a whole turn at far positions. The
 // signed top 32 bits, converted to float32, are the angle in turns within
-// +-1/2, off by at most 2^-26 turns (4e-8 of a turn, 1e-7 rad).
+// +-1/2, off by at most 2^-26 turns (1.5e-8 of a turn, 1e-7 rad).
 //
 // Bound: HBM (each value read and written once). Split: `tpr` lanes share a
 // head row, each with one unit = two chunks of V values that hold V whole pairs

@@ -85,6 +85,18 @@ def rope_frequencies(rot_dim: int, *, theta: float = 10000.0, sections: Optional
     return freqs, axes, gain
 
 
+_PI = 314159265358979323846264338327950288419716939937510582097494459  # 10^62 pi
+
+
+def _turns(f: float) -> int:
+    """round(2^64 f / 2 pi) mod 2^64, as the int64 of the same bits: in whole numbers, for a float64
+    quotient would be off by hundreds of units (and position p turns p times as far)."""
+    num, den = f.as_integer_ratio()
+    num, den = (num << 64) * 10 ** 62, 2 * _PI * den
+    t = (2 * num + den) // (2 * den) % (1 << 64)
+    return t - (1 << 64) if t >= 1 << 63 else t
+
+
 def rope_table(rot_dim: int, *, layout: str = "interleaved", freqs: Optional[Sequence[float]] = None,
                gain: Optional[float] = None, device="cuda", **kw) -> RopeTable:
     """The table of a rotation of the first rot_dim values of each head row, built once.
@@ -106,11 +118,7 @@ def rope_table(rot_dim: int, *, layout: str = "interleaved", freqs: Optional[Seq
     gain = g if gain is None else float(gain)
     if not math.isfinite(gain):
         raise ValueError("gain must be finite")
-    turns = []
-    for x in made:
-        # 2^64 f / 2 pi: a float64 times a power of two, then reduced in whole numbers
-        t = int(math.ldexp(math.fmod(x / (2.0 * math.pi), 1.0), 64)) % (1 << 64)
-        turns.append(t - (1 << 64) if t >= 1 << 63 else t)
+    turns = [_turns(x) for x in made]
     n_axes = 1 + max(axes, default=0)
     n_axes = max(n_axes, len(kw["sections"]) if kw.get("sections") is not None else 1)
     axis = torch.tensor(axes, dtype=torch.uint8).to(device) if n_axes > 1 else None

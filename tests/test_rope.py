@@ -182,3 +182,18 @@ def test_yarn_scales_cos_and_sin_only_for_longer_contexts():
         f, _, g = rope_frequencies(128, scaling="yarn", factor=factor, original=4096)
         assert g == pytest.approx(gain, rel=1e-15)
         assert sla.rope_table(128, scaling="yarn", factor=factor, original=4096, device="cpu").gain == g
+
+
+# 2 pi to 60 digits
+TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+def test_turn_table_is_rounded_once():
+    """Every entry is 2^64 f / 2 pi to the nearest whole number, of the float64 f and of pi itself."""
+    for f in ([0.37 ** i * (7.3 if i == 0 else 1.0) for i in range(32)], rope_frequencies(64)[0],
+              [-1.0, 0.0, 1e-300, 2.0 ** -60, 123456.789, -1e15, 1e300, 0.5]):
+        table = sla.rope_table(2 * len(f), device="cpu", freqs=f)
+        for x, t in zip(f, table.turns.tolist()):
+            off = abs(Fraction(t) - Fraction(x) / TWO_PI * (1 << 64)) % (1 << 64)
+            # (the digits of pi above are off by 1e-61 of it: at 1e300 the turns' fraction is beyond them)
+            assert abs(x) > 1e30 or min(off, (1 << 64) - off) <= Fraction(1, 2) + Fraction(1, 1 << 40), x
