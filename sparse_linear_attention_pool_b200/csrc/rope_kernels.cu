@@ -335,15 +335,14 @@ __global__ void __launch_bounds__(kThreads, NU == 1 ? 3 : 1) norm_rope_bwd_kerne
     for (int j = 0; j < V; ++j) da[k][j] = db[k][j] = 0.0f;
   }
   const unsigned total = unsigned(a.B) * unsigned(a.N), tiles = (total + groups - 1) / groups;
-  constexpr int h0 = 0;
   const int h1 = t.H;
   for (unsigned tile = block; tile < tiles; tile += blocks) {
     const unsigned tok = tile * groups + group;
     const bool live = tok < total;
     const int b = live ? int(tok / unsigned(a.N)) : 0, n = live ? int(tok - unsigned(b) * unsigned(a.N)) : 0;
-    const T* x = static_cast<const T*>(t.x) + b * t.xb + n * t.xn + h0 * t.xh;
-    const T* dy = static_cast<const T*>(t.dy) + b * t.gb + n * t.gn + h0 * t.gh;
-    T* dx = static_cast<T*>(t.y) + b * t.yb + n * t.yn + h0 * t.yh;
+    const T* x = static_cast<const T*>(t.x) + b * t.xb + n * t.xn;
+    const T* dy = static_cast<const T*>(t.dy) + b * t.gb + n * t.gn;
+    T* dx = static_cast<T*>(t.y) + b * t.yb + n * t.yn;
     constexpr int kAhead = NU == 1 && sizeof(T) == 2 ? 2 : 1;  // heads in flight
     Chunk<T, V> rx[kAhead][NU][2], rg[kAhead][NU][2];
     auto fetch = [&](int h, int q) {
@@ -359,12 +358,12 @@ __global__ void __launch_bounds__(kThreads, NU == 1 ? 3 : 1) norm_rope_bwd_kerne
       dy += t.gh;
     };
 #pragma unroll
-    for (int q = 0; q < kAhead; ++q) fetch(h0 + q, q);
+    for (int q = 0; q < kAhead; ++q) fetch(q, q);
     float c[NU][V], s[NU][V];
 #pragma unroll
     for (int k = 0; k < NU; ++k)
       if (live && has[k] && 2 * (lane + k * a.tpr) * V < a.rot) angles<T, V>(a, b, n, lane + k * a.tpr, c[k], s[k]);
-    for (int h = h0; h < h1; h += kAhead) {
+    for (int h = 0; h < h1; h += kAhead) {
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
         if (h + q >= h1) break;  // uniform over the block

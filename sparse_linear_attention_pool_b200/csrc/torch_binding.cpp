@@ -345,14 +345,10 @@ struct NormFunction : torch::autograd::Function<NormFunction> {
     const auto meta = rope_meta(ctx);
     const auto saved = ctx->get_saved_variables();
     const bool need_w = ctx->needs_input_grad(2) || ctx->needs_input_grad(3);
-    for (int i = 0; i < 2; ++i)
-      if (!grads[i].defined()) {
-        auto sizes = saved[i].sizes().vec();
-        if (meta->rows) sizes[2] = *meta->rows;
-        grads[i] = at::zeros(sizes, saved[i].options());
-      }
-    auto [dq, dk, dwq, dwk] = run_norm_backward(saved[0], saved[1], saved[2], saved[3], grads[0], grads[1],
-                                                meta->table, meta->pos.defined() ? saved[4] : Tensor(), meta->eps, meta->N, need_w, {});
+    // (torch hands over zeros for an output that nothing used)
+    auto [dq, dk, dwq, dwk] =
+        run_norm_backward(saved[0], saved[1], saved[2], saved[3], grads[0], grads[1], meta->table,
+                          meta->pos.defined() ? saved[4] : Tensor(), meta->eps, meta->N, need_w, {});
     return {dq, dk, dwq, dwk, Tensor()};
   }
 };

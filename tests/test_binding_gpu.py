@@ -216,3 +216,21 @@ def test_workspaces_are_checked(cuda_lib):
             with pytest.raises(ValueError, match="workspace"):
                 call(bad)
         call(torch.zeros(n, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("rows", [None, 16])
+def test_gradients_where_one_output_is_not_used(cuda_lib, rows):
+    """The other output's gradient counts as zeros, of its own shape."""
+    sla = cuda_lib
+    table = sla.rope_table(64)
+    q, k = randn(2, 4, 9, 64, seed=1), randn(2, 2, 9, 64, seed=2)
+    w = [1 + 0.2 * randn(64, seed=s, dtype=torch.float32) for s in (3, 4)]
+    dy = [randn(2, h, rows or 9, 64, seed=5 + h) for h in (4, 2)]
+    for i in range(2):
+        leaves = [t.detach().requires_grad_(True) for t in (q, k, *w)]
+        y = sla.qk_norm_rope(*leaves, table, N=7, rows=rows)
+        got = torch.autograd.grad(y[i], leaves, dy[i])
+        zero = [g if i == j else torch.zeros_like(g) for j, g in enumerate(dy)]
+        want = sla.qk_norm_rope_backward(q, k, *w, *zero, table, N=7)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert (got[1 - i] == 0).all() and (got[3 - i] == 0).all() and got[i].any() and got[2 + i].any()
