@@ -234,3 +234,40 @@ def test_gradients_where_one_output_is_not_used(cuda_lib, rows):
         want = sla.qk_norm_rope_backward(q, k, *w, *zero, table, N=7)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert (got[1 - i] == 0).all() and (got[3 - i] == 0).all() and got[i].any() and got[2 + i].any()
+
+
+FIRST_CALL = """
+import torch
+import sparse_linear_attention_pool_b200 as sla
+x, w = torch.randn(40, 2, 64, device="cuda").bfloat16(), torch.ones(64, device="cuda", dtype=torch.bfloat16)
+k = torch.zeros(9000, 2, 64, device="cuda", dtype=torch.bfloat16)
+plan, table = sla.prompt_plan([40], Hq=2, Hkv=2, d=64), sla.rope_table(64)
+one = sla.prompt_plan([1], [9000], Hq=2, Hkv=2, d=64)
+
+
+def step():
+    q, h = sla.qk_norm_rope(x, x, w, w, table)
+    o, lse, rest = sla.prompt_forward(q, h, x, plan, want_rest=True)
+    dq, dk, dv = sla.prompt_backward(q, h, x, o, lse, x, plan, rest=rest)
+    return (o, dv, sla.rope(x, table), sla.prompt_attention(q[:1], k, k, one), *sla.qk_norm_rope_backward(x, x, w, w, dq, dk, table))
+
+
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    made = step()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(made, step()))
+print("same")
+"""
+
+
+def test_first_call_of_a_process_is_captured(cuda_lib):
+    """A capture needs no call before it that loads the kernels."""
+    import os
+    import subprocess
+    import sys
+
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]

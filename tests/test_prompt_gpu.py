@@ -562,3 +562,90 @@ def test_a_nan_query_makes_its_keys_gradients_nan(cuda_lib, d):
         dq, dk, dv = grads(bad)
         assert dq[r].isnan().all() and dk[:r + 1].isnan().all() and dv[:r + 1].isnan().all(), r
         assert torch.equal(dv[r + 1:], clean[2][r + 1:]), r
+
+
+def scores_size(q, k, lq, lk, scale):
+    """Per query row: the largest scale sum_i |q_i k_i| over its sequence's keys (what a score's rounding is relative to)."""
+    out = torch.zeros(q.shape[:2], dtype=torch.float64)
+    a = b = 0
+    for n, m in zip(lq, lk):
+        for h in range(q.shape[1]):
+            if n and m:
+                kh = k[b:b + m, h // (q.shape[1] // k.shape[1])].double().abs()
+                out[a:a + n, h] = (q[a:a + n, h].double().abs() @ kh.t()).amax(-1) * scale
+        a, b = a + n, b + m
+    return out
+
+
+def lse_bound(case, q, k, lse, scale=None):
+    """Row by row. A score: float32 sums of d products, 2 d + 4 half-steps of its own size. The
+    exponentials: the hardware's 2^-22 of each; at d = 64 a quarter of them by a cubic, 1.0e-4. Their
+    sum: eight interleaved chains over the keys, half a step an addition, and a few to join them
+    (split keys: fewer). log2 and the product with ln 2: 2^-22 of the result each."""
+    lq, lk, _, _, d, _ = case
+    lk = lq if lk is None else lk
+    e = (2 * d + 4) * R.EPS32 * scores_size(q, k, lq, lk, 1 / math.sqrt(d) if scale is None else scale)
+    return e + (1.05e-4 if d == 64 else 0.0) + 2.0 ** -22 + (max(lk) / 8 + 24) * R.EPS32 + 2.0 ** -21 * (1 + lse.abs())
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_lse_row_by_row(cuda_lib, case):
+    sla = cuda_lib
+    q, k, v, _, lq, lk = make(case, seed=15)
+    _, lse = sla.prompt_forward(q.cuda(), k.cuda(), v.cuda(), plan_of(sla, case))
+    want = R.prompt(q, k, v, lq, lk, case[5])["lse"]
+    got, fin = lse.cpu().double(), want != -math.inf
+    assert torch.equal(got == -math.inf, ~fin)
+    err, bound = (got - want).abs()[fin], lse_bound(case, q, k, want)[fin]
+    assert (err <= bound).all(), (err / bound).max()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tokens", [1, 3])
+def test_every_key_at_the_edge_of_a_piece_counts_once(cuda_lib, d, tokens):
+    """Long rows whose keys are split: query head i looks for one key, in turn the first and the
+    last of each piece and the sequence's last. Left out, O is another row of V; counted twice,
+    lse is off by ln 2."""
+    from tests.test_prompt import read
+
+    sla = cuda_lib
+    n, H = 9000 + 37, 32
+    case = ([tokens], [n], H, 1, d, False)
+    plan = plan_of(sla, case)
+    items = read(plan)[1]
+    assert any(it["slot"] >= 0 for it in items)
+    edges = sorted({min(n, e) - s for it in items for e, s in ((it["b0"] * 128, 0), (it["b1"] * 128, 1))} | {n - 1})
+    g = torch.Generator().manual_seed(16)
+    v = torch.randn(n, 1, d, generator=g).bfloat16()
+    for at in range(0, len(edges), H):
+        want = edges[at:at + H]
+        # key want[i] is 32 along axis i, query head i 16 sqrt(d) / 16 along it: a score of 32 against 0
+        q, k = torch.zeros(tokens, H, d), torch.zeros(n, 1, d)
+        for i, j in enumerate(want):
+            q[:, i, i], k[j, 0, i] = math.sqrt(d), 32.0
+        q, k = q.bfloat16(), k.bfloat16()
+        o, lse = sla.prompt_forward(q.cuda(), k.cuda(), v.cuda(), plan)
+        ref = R.prompt(q, k, v, [tokens], [n], False)
+        check_forward(case, o, None, ref, q, k)
+        err = (lse.cpu().double() - ref["lse"]).abs()
+        assert (err <= lse_bound(case, q, k, ref["lse"])).all(), err.max()
+        # one key carries all but n e^-30 of the row
+        for i, j in enumerate(want):
+            assert ((o[:, i].cpu().float() - v[j, 0].float()).abs() <= 2.0 ** -8 * v[j, 0].float().abs() + 1e-6).all(), j
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("case", [([700], None, 2, 1, 64), ([1], [9000], 8, 1, 64), ([1], [9000], 8, 1, 128), ([3000], None, 8, 8, 64)],
+                         ids=str)
+def test_growing_maxima_in_every_form(cuda_lib, case, causal):
+    """The running maximum raised in every block, where heads are of 64 (whose scores have columns
+    of their own), where keys are split, and with one and two tiles to an item."""
+    sla = cuda_lib
+    case = (*case, causal)
+    lk = case[1] or case[0]
+    q, k, v, _, lq, lk = make(case, seed=17)
+    q[..., 0], k[:, :, 0] = 8.0, torch.linspace(120.0, 0.0, lk[0])[:, None].bfloat16()
+    o, lse = sla.prompt_forward(q.cuda(), k.cuda(), v.cuda(), plan_of(sla, case))
+    ref = R.prompt(q, k, v, lq, lk, causal)
+    check_forward(case, o, lse, ref, q, k)
+    assert ((lse.cpu().double() - ref["lse"]).abs() <= lse_bound(case, q, k, ref["lse"])).all()
