@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(320, 1)
       for (int j = 0; j < 64; j += 2) {  // 2^(c S - lse2)
         const uint64_t x = mul2(two(p[j], p[j + 1]), c2);
         if ((j >> 1) % 8 >= 8 - C::kFmaPairs) {
-          ex2_fma(x, p[j], p[j + 1]);
+          ex2_fma<true>(x, p[j], p[j + 1]);  // (a NaN query's column holds NaN for every key that it sees)
         } else {
           untwo(x, p[j], p[j + 1]);
           p[j] = ex2(p[j]);

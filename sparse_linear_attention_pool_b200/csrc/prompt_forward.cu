@@ -81,6 +81,11 @@ struct FwdCfg {
   // 675 us, one pair 658, two 635, three 669. At d = 128 (32768 tokens, 12 heads) the
   // power limit sets the clock and every other count is slower: none 2400 us, two 2430.
   static constexpr int kFmaPairs = D == 64 ? 2 : 0;
+  // In what way they treat NaN: one tile's warps feel the operation that keeping it costs
+  // (8192 full tokens, 16 heads: 372 us, and 357 without), those of two do not (16384 causal
+  // ones: 651, and 660). NaN scores make the row's maximum NaN and so the other columns; a row
+  // with an infinite one alone is made NaN at its end.
+  static constexpr bool kNan = TILES == 2;
   // TMEM columns: S of every tile (128 each), O of every tile (D each).
   // P takes the first 64 columns of its S at d = 128, where TMEM is full: the next S
   // waits for P V. At d = 64 it has columns of its own, so the next S is formed as soon
@@ -481,7 +486,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, FEW>::kThreads, FwdCfg<D, TIL
           for (int j = from; j < to; j += 2) {
             const uint64_t x = fma2(two(s[j], s[j + 1]), c2, mc2);
             if ((j >> 1) % 8 >= 8 - C::kFmaPairs) {
-              ex2_fma(x, s[j], s[j + 1]);
+              ex2_fma<C::kNan>(x, s[j], s[j + 1]);
             } else {
               untwo(x, s[j], s[j + 1]);
               s[j] = ex2(s[j]);
@@ -518,6 +523,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, FEW>::kThreads, FwdCfg<D, TIL
         wait_w(bO0 + t, (done + steps - 1) & 1);
         tc_fence_after();
       }
+      if (!C::kNan && m == INFINITY) l = NAN;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const PromptItem& at = C::kAgain ? *cur : w.it;
       const int slot = at.slot;

@@ -99,15 +99,17 @@ __device__ __forceinline__ uint4 three_bf16(float x) {
   return make_uint4(pack_bf16(a, b), pack_bf16(y - b, 0.0f), 0, 0);
 }
 // 2^x of two values on the FMA units, for x <= 127: x = i + f with i the nearest
-// whole number (adding 1.5 2^23 rounds to it; 127 more make it the exponent field of
-// 2^i), 2^f by a cubic with p(0) = 1 fitted to the least relative error on
-// [-1/2, 1/2] (1.0e-4, a twentieth of a bf16 step), times 2^i, whose field at i = -127
-// is 0: x <= -127 gives 0. The product keeps NaN (i added to the bits of 2^f would make it a number).
+// whole number (adding 1.5 2^23 rounds to it), 2^f by a cubic with p(0) = 1 fitted
+// to the least relative error on [-1/2, 1/2] (1.0e-4, a twentieth of a bf16 step).
+// x <= -127 gives 0. kNan: times 2^i (127 more on the way make i the exponent field
+// of 2^i), which keeps NaN; else i is added to the exponent of 2^f, an operation
+// less, and NaN comes out as a number near the largest.
+template <bool kNan>
 __device__ __forceinline__ void ex2_fma(uint64_t x2, float& lo, float& hi) {
   float x, y;
   untwo(x2, x, y);
   const uint64_t v = two(max_nan(x, -127.0f), max_nan(y, -127.0f));
-  constexpr float kRound = 12582912.0f + 127.0f;
+  constexpr float kRound = 12582912.0f + (kNan ? 127.0f : 0.0f);
   const uint64_t t = add2(v, two(kRound, kRound));
   const uint64_t f = fma2(add2(t, two(-kRound, -kRound)), two(-1.0f, -1.0f), v);
   uint64_t p = fma2(f, two(0.05500893294811249f, 0.05500893294811249f), two(0.2422109693288803f, 0.2422109693288803f));
@@ -115,7 +117,15 @@ __device__ __forceinline__ void ex2_fma(uint64_t x2, float& lo, float& hi) {
   p = fma2(p, f, two(1.0f, 1.0f));
   float i, j;
   untwo(t, i, j);
-  untwo(mul2(p, two(__int_as_float(__float_as_int(i) << 23), __int_as_float(__float_as_int(j) << 23))), lo, hi);
+  const int ei = __float_as_int(i) << 23, ej = __float_as_int(j) << 23;
+  if (kNan) {
+    untwo(mul2(p, two(__int_as_float(ei), __int_as_float(ej))), lo, hi);
+  } else {
+    float a, b;
+    untwo(p, a, b);
+    lo = __int_as_float(__float_as_int(a) + ei);
+    hi = __int_as_float(__float_as_int(b) + ej);
+  }
 }
 
 // Taking over a block of the grid that has not started (one thread asks; blocks are handed

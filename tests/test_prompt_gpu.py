@@ -649,3 +649,25 @@ def test_growing_maxima_in_every_form(cuda_lib, case, causal):
     ref = R.prompt(q, k, v, lq, lk, causal)
     check_forward(case, o, lse, ref, q, k)
     assert ((lse.cpu().double() - ref["lse"]).abs() <= lse_bound(case, q, k, ref["lse"])).all()
+
+
+@pytest.mark.parametrize("case", [([3000], None, 8, 8, 64, True), ([3000], None, 8, 8, 128, True), ([300], None, 2, 2, 64, True),
+                                  ([1], [9000], 2, 2, 64, True), ([4], [9000], 2, 2, 128, True)], ids=IDS)
+def test_one_infinite_score_in_every_form(cuda_lib, case):
+    """One and two tiles to an item, whole and split keys: the rows that see the key are NaN (their lse
+    too), the others as they were."""
+    sla = cuda_lib
+    q, k, v, _, lq, lk = make(case, seed=23)
+    q[..., 0] = 1.0
+    plan = plan_of(sla, case)
+    want = sla.prompt_forward(q.cuda(), k.cuda(), v.cuda(), plan)
+    first = max(0, lk[0] - 2000)
+    for j in range(first, first + 16):
+        bad = k.clone()
+        bad[j, 0, 0] = math.inf
+        see = torch.zeros(case[2], sum(lq), dtype=torch.bool)
+        see[0] = torch.arange(lq[0]) + lk[0] - lq[0] >= j
+        o, lse = (t.cpu() for t in sla.prompt_forward(q.cuda(), bad.cuda(), v.cuda(), plan))
+        assert o.transpose(0, 1)[see].isnan().all() and lse.t()[see].isnan().all(), j
+        assert torch.equal(o.transpose(0, 1)[~see], want[0].cpu().transpose(0, 1)[~see])
+        assert torch.equal(lse.t()[~see], want[1].cpu().t()[~see])
