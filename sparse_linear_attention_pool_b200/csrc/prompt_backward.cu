@@ -87,7 +87,10 @@ __global__ void __launch_bounds__(256) prompt_rowsum_kernel(const PromptGradDev 
 // as three bf16 that add up to its float32, gives S - lse / scale and dP - D.
 // Warps 0-3 form columns 0-63 of P^T and dS^T, warps 4-7 columns 64-127; warp 8
 // loads, warp 9 issues. While the tensor cores run dV_i and S^T_{i+1} the warps
-// form dS_i, while they run dK_i and dP^T_{i+1} the warps form P_{i+1}.
+// form dS_i, while they run dK_i and dP^T_{i+1} the warps form P_{i+1}. P is formed as the
+// row kernel forms it, on the special function units alone: a share on the FMA units (the
+// forward's at d = 64) made no difference (16384 causal tokens, 12 heads of 128: 2218 us, and
+// 2220 with three of eight pairs; 1732 tokens: 51.3 and 50.8).
 // Bound: the tensor cores at d = 128 (8192 causal tokens, 16 heads: 452 us, the tensor pipe
 // 68 % busy); at d = 64 the chain S - P - dP - dS of one key tile (347 us, 46 %).
 // ---------------------------------------------------------------------------
@@ -105,10 +108,6 @@ struct KeyCfg {
   static constexpr int oL = oOne + kStep;                 // B of S and of dP, per stage
   static constexpr int kBytes = oL + kStages * 2 * kStep;
   static constexpr int kSmem = kBytes + 1024;
-  // Of every 8 pairs of exponentials, formed on the FMA units. Measured, backward of 14693
-  // tokens, 16 + 4 heads, d = 128: none 1032 us, two 1012, three 997, four 1020; of 8192
-  // tokens, 16 heads, d = 64: none 575 us, two 597, three 604.
-  static constexpr int kFmaPairs = D == 64 ? 0 : 3;
   // TMEM columns. At d = 64 there is room for a second S, so that the next tile's S is
   // formed while this one's P is in use (a tile takes 2280 clocks instead of 2620).
   static constexpr bool kTwoS = D == 64;
@@ -358,14 +357,9 @@ __global__ void __launch_bounds__(320, 1)
       tmem_wait_ld();
 #pragma unroll
       for (int j = 0; j < 64; j += 2) {  // 2^(c S - lse2)
-        const uint64_t x = mul2(two(p[j], p[j + 1]), c2);
-        if ((j >> 1) % 8 >= 8 - C::kFmaPairs) {
-          ex2_fma<true>(x, p[j], p[j + 1]);  // (a NaN query's column holds NaN for every key that it sees)
-        } else {
-          untwo(x, p[j], p[j + 1]);
-          p[j] = ex2(p[j]);
-          p[j + 1] = ex2(p[j + 1]);
-        }
+        untwo(mul2(two(p[j], p[j + 1]), c2), p[j], p[j + 1]);
+        p[j] = ex2(p[j]);
+        p[j + 1] = ex2(p[j + 1]);
       }
       if (__any_sync(0xffffffffu, masked)) {
 #pragma unroll
