@@ -408,12 +408,15 @@ sla_status sla_qk_norm_rope_backward(const sla_heads* q, const sla_heads* k, con
  * nor written, and no sequence reads another's rows into its results (they may
  * hold NaN). Within a sequence, a key or value row that is not finite reaches
  * every query that sees it, and may reach queries before it in the same block of
- * 128 keys.
+ * 128 keys. A query with a score of NaN or plus infinity gets NaN, in lse too.
+ * In the backward a q or dO row that is not finite reaches the gradients of the keys that
+ * it sees, and may reach those of up to 255 keys behind them.
  *
  * The sequences' lengths are planned once on the host: a plan lists the kernels'
  * work items, the longest first. sla_prompt_plan writes it to host memory; the
  * caller copies the same bytes to the device (256-byte aligned) and passes both.
- * One plan serves any number of calls, also at the same time; only the device
+ * One plan serves any number of calls, also at the same time, and a captured graph
+ * reads it at every replay; only the device
  * copy's status word (sla_read_device_status(plan_device, stream)) is written to,
  * and only when a bounded in-kernel wait expires or an item is out of range. */
 typedef struct sla_prompt_params {
@@ -445,8 +448,9 @@ size_t sla_prompt_plan_used(const void* plan);
  * where few rows read long caches, whose keys are then split among blocks). */
 size_t sla_prompt_workspace_size(const void* plan);
 
-/* O and, for the backward, where they are not NULL:
- *   lse   [Tq, Hq] float32 = log sum exp(scale q.k) over the keys that each query sees;
+/* O, which overlaps no input, and for the backward, where they are not NULL:
+ *   lse   [Tq, Hq] float32 = log sum exp(scale q.k) over the keys that each query sees
+ *         (d = 64: a quarter of the exponentials are good to 1e-4, and so is the sum);
  *   rest  [Tq, Hq, d] bf16, 16-byte aligned = what O's rounding left off: with it the
  *         gradients' row sums dO.O are those of the float32 O. */
 sla_status sla_prompt_forward(const sla_rows* q, const sla_rows* k, const sla_rows* v, const sla_rows* o, float* lse,

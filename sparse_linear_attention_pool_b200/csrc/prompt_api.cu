@@ -152,10 +152,10 @@ constexpr double kNextCost = 1.2;
 constexpr double kJoinCost = 3.0;  // the second launch
 // A step of a one-tile item, two of which share an SM, and of one that has its SM to
 // itself. At d = 128 the second copy of the keys costs bandwidth to shared memory (4096
-// causal tokens, 16 heads: 82 us as one-tile items, 58 as two-tile ones). At d = 64 the
-// exponentials bound both, and the items' ends decide (8192 causal tokens, 16 heads: 186
-// and 177 us; 4096: 61 and 53), or the last round (8192 full ones, whose two-tile items
-// leave half of it idle, while the last one-tile items have an SM each: 356 and 414).
+// causal tokens, 16 heads: 84 us as one-tile items, 60 as two-tile ones). At d = 64 the
+// softmax bounds both, and the items' ends decide (8192 causal tokens, 16 heads: 188
+// and 177 us; 4096: 63 and 52), or the last round (8192 full ones, whose two-tile items
+// leave half of it idle, while the last one-tile items have an SM each: 357 and 417).
 double one_tile_step(int d, bool shared) { return shared ? (d == 128 ? 1.4 : 1.02) : (d == 128 ? 0.9 : 0.7); }
 
 // full_rows: how full of live rows the tiles are

@@ -91,8 +91,9 @@ __global__ void __launch_bounds__(256) prompt_rowsum_kernel(const PromptGradDev 
 // row kernel forms it, on the special function units alone: a share on the FMA units (the
 // forward's at d = 64) made no difference (16384 causal tokens, 12 heads of 128: 2218 us, and
 // 2220 with three of eight pairs; 1732 tokens: 51.3 and 50.8).
-// Bound: the tensor cores at d = 128 (8192 causal tokens, 16 heads: 452 us, the tensor pipe
-// 68 % busy); at d = 64 the chain S - P - dP - dS of one key tile (347 us, 46 %).
+// Bound: the tensor cores at d = 128 (8192 causal tokens, 16 heads: 475 us, the tensor pipe
+// 64 % busy); at d = 64 the chain S - P - dP - dS of one key tile, which waits for itself
+// (344 us: tensor pipe 46 %, special function units 42 %, issue slots 33 %).
 // ---------------------------------------------------------------------------
 namespace {
 
@@ -468,8 +469,8 @@ __global__ void __launch_bounds__(128) prompt_keys_join_kernel(const PromptGradD
 //   dQ += dS K_j (M = 128, N = d, K = 128; A in TMEM).
 // One 128-column region X per tile leaves TMEM room for two tiles' dQ: the chain
 // S - dP - dS - dQ of one tile runs in the gaps of the other's. Measured, 8192 causal
-// tokens, 16 heads: d = 128, 325 us, the tensor pipe 67 % busy (its bound); d = 64, 268 us,
-// the special function units 54 % (the chain is the bound).
+// tokens, 16 heads: d = 128, 328 us, the tensor pipe 66 % busy (its bound); d = 64, 272 us, no
+// unit at its limit (special function units 54 %, tensor pipe 39 %, issue slots 36 %): the chain.
 // ---------------------------------------------------------------------------
 namespace {
 

@@ -20,12 +20,18 @@
 // queries and first keys while this one's last steps run. Measured: 6 sequences of 310 to
 // 8191 tokens, 32 / 8 heads of 128, 604 us (with a block per item 670); 16 of 1000
 // tokens, 16 / 4 heads of 64, 74 us (86).
+// (Figures in this file: the same inputs call after call, 60 ms at a time, other GPUs up to
+// 4 % off. In long runs on changing inputs the power limit sets a lower clock: 685 to 705 us
+// for the first of these.)
 // Every wait is bounded; the kernel drains its copies and MMAs before it ends.
 //
 // Bound: at d = 128 the tensor cores under the power limit (32768 causal tokens, 12
-// heads: 2730 us, 1.21 PFLOP/s, 72 % of cuBLAS's burst rate and 87 % of its sustained
-// one); at d = 64 the special function units (16384 causal tokens, 16 heads: 660 us);
-// with 32 rows or fewer the keys' bytes (single tokens over caches: 5.6 TB/s).
+// heads: 2500 us at 1.49 GHz, 1.32 PFLOP/s, 80 % of cuBLAS's burst rate; in a long run 2840 us,
+// 1.16 PFLOP/s, 83 % of its sustained one); at d = 64 no unit by itself (16384 causal
+// tokens, 16 heads: 650 us; of 8192, special function units 55 %, issue slots 50 %, tensor pipe
+// 35 %): a scheduler has two softmax warps, and each waits for its own S, maximum and
+// exponentials in turn; with 32 rows or fewer the keys' bytes (single tokens over caches:
+// 5.4 TB/s in the kernel).
 #include <string.h>
 
 #include "prompt_tc.cuh"
@@ -78,8 +84,8 @@ struct FwdCfg {
   // Of every 8 pairs of exponents, this many are formed on the FMA units: the special
   // function units take 1024 clocks for a tile's exponentials, its products take 512
   // (d = 64) or 1024 (d = 128). Measured, 16384 causal tokens, 16 heads, d = 64: none
-  // 675 us, one pair 658, two 635, three 669. At d = 128 (32768 tokens, 12 heads) the
-  // power limit sets the clock and every other count is slower: none 2400 us, two 2430.
+  // 711 us, one pair 675, two 650, three 665; 8192 full ones (one tile): 372, 377, 358, 358.
+  // At d = 128 (32768 tokens, 12 heads) the power limit sets the clock: none 2530 us, two 2560.
   static constexpr int kFmaPairs = D == 64 ? 2 : 0;
   // In what way they treat NaN: one tile's warps feel the operation that keeping it costs
   // (8192 full tokens, 16 heads: 372 us, and 357 without), those of two do not (16384 causal
@@ -592,8 +598,8 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, FEW>::kThreads, FwdCfg<D, TIL
 // W warps per row (four rows, or one, per block): each finds the weights 2^(L_i - M)
 // and adds up every W-th part (a part's O row is one 16- or 8-byte load per lane); the
 // W sums are added in order. Bound: latency. Four warps where rows have many parts: a
-// single-token call over 100000 keys, 37 parts, takes 73 us, and 86 with one; one warp
-// where many rows have a few: a 1732-token batch, two parts, takes 17 us, and 23 with four.
+// single-token call over 100000 keys, 37 parts, takes 75 us, and 79 with one; one warp
+// where many rows have a few: 3000 tokens, 8 heads of 64, two parts, take 35 us, and 44 with four.
 template <int D, int W>
 __global__ void __launch_bounds__(128) prompt_join_kernel(const PromptDev a) {
   constexpr int V = D / 32;

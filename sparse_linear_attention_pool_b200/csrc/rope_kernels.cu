@@ -311,8 +311,10 @@ __global__ void __launch_bounds__(kThreads, NU == 1 ? 4 : 2) rope_kernel(const R
 // One round of blocks, shared between q and k by their heads, walks over token
 // tiles; each block keeps its dw in registers and leaves one row of partial sums,
 // which norm_dw_kernel adds in a fixed order.
-// Bound: HBM and the issue of the float32 arithmetic (54 % of the issue slots). Measured, queries and keys of 32760 tokens, 12 heads of 128: 145 us, 4.1 TB/s
-// (600 MB that it reads and writes).
+// Bound: latency, neither HBM nor issue by itself: of each head a block waits for its loads and
+// for two chains of shuffles, with 24 warps to an SM. Measured, queries and keys of 32760 tokens,
+// 12 heads of 128: 146 us, 4.1 TB/s (600 MB that it reads and writes; 63 % of a copy's rate), 58 %
+// of the issue slots.
 template <typename T, int V, int NU, bool HALF>
 __global__ void __launch_bounds__(kThreads, NU == 1 ? 3 : 1) norm_rope_bwd_kernel(const RopeArgs a) {
   extern __shared__ float dw_sh[];  // [groups][d]
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, NU == 1 ? 3 : 1) norm_rope_bwd_kerne
 
 // dw[i] = sum of the blocks' partial rows, in a fixed order: 32 slices of rows per
 // column, then the slices. One block per 32 columns of one tensor. Bound: latency
-// (7.5 us by itself for 444 rows of 128; started beside the kernel before it).
+// (7.7 us by itself for 444 rows of 128; started beside the kernel before it).
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const RopeArgs a, int rows) {
   __shared__ float part[32][33];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial rows are written

@@ -51,7 +51,9 @@ def _lengths(lens, what):
 def prompt_plan(lens_q: Sequence[int], lens_k: Optional[Sequence[int]] = None, *, Hq: int, Hkv: int, d: int,
                 causal: bool = True, softmax_scale: float = 0.0, grad: Optional[bool] = None, device="cuda") -> PromptPlan:
     """Plans the attention of sequences of lens_q query tokens over lens_k keys (default:
-    the same lengths). Made once for a batch of lengths, and good for any number of calls.
+    the same lengths). Made once for a batch of lengths, and good for any number of calls (a
+    model's layers; a decoding step, whose caches have grown, needs one of its own). Keep it as
+    long as a captured graph that reads it.
     softmax_scale 0 selects 1 / sqrt(d). grad: whether the plan serves the backward pass too
     (default: for whole prompts, where lens_k is not given)."""
     lens_q = _lengths(lens_q, "lens_q")
@@ -108,7 +110,8 @@ def prompt_backward(q, k, v, o, lse, do, plan: PromptPlan, *, rest=None, out=Non
 
 
 def prompt_attention(q, k, v, plan: PromptPlan, *, stream=None):
-    """O = softmax(scale Q K^T + mask) V for the plan's packed sequences, [rows of q, Hq, d].
+    """O = softmax(scale Q K^T + mask) V for the plan's packed sequences, [rows of q, Hq, d]; rows
+    behind the plan's last token are not written.
     Differentiable in q, k and v (with a plan made for it), in reverse mode."""
     if stream is not None:
         with on_stream(stream, q.device, q, k, v):

@@ -99,7 +99,8 @@ def _turns(f: float) -> int:
 
 def rope_table(rot_dim: int, *, layout: str = "interleaved", freqs: Optional[Sequence[float]] = None,
                gain: Optional[float] = None, device="cuda", **kw) -> RopeTable:
-    """The table of a rotation of the first rot_dim values of each head row, built once.
+    """The table of a rotation of the first rot_dim values of each head row, built once (and kept
+    as long as a captured graph that reads it).
 
     layout "interleaved": pair i is (x[2i], x[2i+1]); "half": (x[i], x[i + rot_dim/2]).
     The other arguments are rope_frequencies'; `freqs` (radians per position, rot_dim / 2
