@@ -132,6 +132,8 @@ def on_stream(stream, device, *used):
     memory of the tensors `used` is not handed out again before that stream is done with it."""
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError(f"stream: of {stream.device}, the tensors are on {device}")
     for t in used:
         if isinstance(t, (tuple, list)):
             on_stream(stream, device, *t)

@@ -197,3 +197,22 @@ def test_turn_table_is_rounded_once():
             off = abs(Fraction(t) - Fraction(x) / TWO_PI * (1 << 64)) % (1 << 64)
             # (the digits of pi above are off by 1e-61 of it: at 1e300 the turns' fraction is beyond them)
             assert abs(x) > 1e30 or min(off, (1 << 64) - off) <= Fraction(1, 2) + Fraction(1, 1 << 40), x
+
+
+def test_a_stream_of_another_device_is_refused():
+    """The call would run on the tensors' device, in no order with that stream."""
+    class Stream:
+        cuda_stream, device = 1, torch.device("cuda", 1)
+
+    from sparse_linear_attention_pool_b200.rotary import on_stream
+
+    with pytest.raises(ValueError, match="stream"):
+        on_stream(Stream(), torch.device("cuda", 0))
+    x, w = torch.zeros(4, 1, 64, dtype=torch.bfloat16), torch.ones(64)
+    table, plan = sla.rope_table(64, device="cpu"), sla.prompt_plan([4], Hq=1, Hkv=1, d=64, device="cpu")
+    for call in (lambda s: sla.rope(x, table, stream=s), lambda s: sla.qk_norm_rope(x, x, w, w, stream=s),
+                 lambda s: sla.qk_norm_rope_backward(x, x, w, w, x, x, stream=s),
+                 lambda s: sla.prompt_attention(x, x, x, plan, stream=s), lambda s: sla.prompt_forward(x, x, x, plan, stream=s),
+                 lambda s: sla.prompt_backward(x, x, x, x, torch.zeros(4, 1), x, plan, stream=s)):
+        with pytest.raises(ValueError, match="stream"):
+            call(Stream())
